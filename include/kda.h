@@ -446,6 +446,90 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
                      int *dev_status, void *stream);
 
 /*
+ * Linear attention with one decay per head:
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,    o_t = scale S_t^T q_t
+ *
+ * for every (sequence, head), with a scalar log-decay g_t. Layouts, states,
+ * packed batches, ownership, alignment and errors as above (q, k [B, T, H, dk],
+ * v, o [B, T, H, dv], states fp32 [N, H, dv, dk]); there is no beta, k and q
+ * need no normalisation, and nothing bounds g from below.
+ *
+ *   gate   : KDA_HLA_GATE_TOKEN: g [B, T, H] of type dtype, one log-decay per
+ *            token and head; KDA_HLA_GATE_HEAD: g fp32 [H], the same for every
+ *            token (a fixed number: it has no gradient). Documented, not
+ *            checked: g <= 0 (a positive g grows the state). A g below -138
+ *            (-infinity too) empties the state.
+ *   S0     : the states before the first token, or NULL (zeros). S_T: the
+ *            states after the last token, or NULL. A sequence without tokens
+ *            has S_T = S0.
+ *   cu_seqlens : device int32 [num_seqs + 1] (B must be 1, T is the total) or
+ *            NULL (num_seqs is then ignored). Tokens before the first or
+ *            behind the last sequence are neither read nor written. Offsets
+ *            are clamped to [0, T].
+ *   workspace : the states at the chunks' borders; kda_hla_*_workspace_size
+ *            (num_seqs 0: a dense batch) gives the bytes, (size_t)-1 for sizes
+ *            that the call would refuse. One workspace serves one call at a
+ *            time.
+ *   dev_status : NULL, or a device int set to KDA_ERR_TIMEOUT if a bounded
+ *            wait of a tensor-core kernel gives up.
+ *   path   : KDA_PATH_AUTO or KDA_PATH_SIMT (kda_path).
+ *
+ * Arithmetic: sums, states and decays in fp32 (the decays' sums in fp64).
+ *
+ * kda_hla_backward: the gradients of q, k, v, g and S0 from dO, the outputs'
+ * (dtype, [B, T, H, dv]), and dS_T, the last states' (fp32, or NULL: zeros).
+ * dq, dk_out [B, T, H, dk] and dv_out [B, T, H, dv] (dtype) are always written;
+ * dg ([B, T, H], dtype; KDA_HLA_GATE_TOKEN only) and dS0 (fp32) may be NULL.
+ * The gradients of a packed batch's tokens outside its sequences are set to zero.
+ * The states are computed again from the inputs: nothing of the forward call is
+ * needed. Results do not depend on the order in which blocks run.
+ */
+typedef enum { KDA_HLA_GATE_TOKEN = 0, KDA_HLA_GATE_HEAD = 1 } kda_hla_gate;
+
+size_t kda_hla_forward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype, int path);
+int kda_hla_forward(const void *q, const void *k, const void *v, const void *g, const float *S0, void *o, float *S_T,
+                    int B, int T, int H, int dk, int dv, float scale, int dtype, int gate, const int32_t *cu_seqlens,
+                    int num_seqs, void *workspace, size_t workspace_bytes, int *dev_status, void *stream, int path);
+size_t kda_hla_backward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype, int path);
+int kda_hla_backward(const void *q, const void *k, const void *v, const void *g, const float *S0, const void *dO,
+                     const float *dS_T, void *dq, void *dk_out, void *dv_out, void *dg, float *dS0, int B, int T, int H,
+                     int dk, int dv, float scale, int dtype, int gate, const int32_t *cu_seqlens, int num_seqs,
+                     void *workspace, size_t workspace_bytes, int *dev_status, void *stream, int path);
+
+/*
+ * One token of the same recurrence for each of N requests, the states updated
+ * in place: q, k [N, H, dk], v, o [N, H, dv], g [N, H] (or fp32 [H] with
+ * KDA_HLA_GATE_HEAD), S [N, H, dv, dk] fp32.
+ */
+int kda_hla_decode_step(const void *q, const void *k, const void *v, const void *g, float *S, void *o, int N, int H,
+                        int dk, int dv, float scale, int dtype, int gate, void *stream);
+
+/*
+ * Rotary positions for q [B, T, Hq, d] and k [B, T, Hk, d] (k NULL and Hk 0: q
+ * alone): over the first rot_dim channels of every head, pair i turns by the
+ * angle x = position * inv_freq[i],
+ *
+ *     (a, b) -> mscale (a cos x - b sin x, b cos x + a sin x),
+ *
+ * the other channels pass through. Pair i is the channels (i, i + rot_dim / 2),
+ * or (2i, 2i + 1) when `interleaved`. `inverse` turns by -x: with the same
+ * mscale that is the transposed map, which takes the gradients of the outputs
+ * to those of the inputs.
+ *
+ *   positions : device [B, T], int32 or (positions_64bit) int64, or NULL: 0 ..
+ *            T - 1 in every sequence. Any value is allowed: angles are reduced
+ *            in fp64.
+ *   inv_freq  : device fp32 [rot_dim / 2].
+ *   q_out, k_out : as q, k; they may be q and k themselves (in place) but must
+ *            not overlap them otherwise.
+ *   Sizes  : d even, at most 1024; rot_dim even, 2 .. d.
+ */
+int kda_rope(const void *q, const void *k, const void *positions, int positions_64bit, const float *inv_freq, void *q_out,
+             void *k_out, int B, int T, int Hq, int Hk, int d, int rot_dim, int interleaved, int inverse, float mscale,
+             int dtype, void *stream);
+
+/*
  * Diagnostic: one CTA waits, through the same bounded-wait helpers the
  * tensor-core prefill uses, on an mbarrier that nothing arrives on (every wait
  * on a copy or an MMA) and then on a flag in global memory that nothing sets

@@ -1,0 +1,179 @@
+// Linear attention with one decay per head, shared by its kernels:
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t      (per sequence and head)
+// with a scalar log-decay g_t. States are fp32 [N, H, dv, dk] (S^T row-major), as everywhere in
+// the library.
+//
+// Chunked form. Within a chunk of C tokens, G_r = g_1 + .. + g_r from the chunk's start and
+// D_rs = e^{G_r - G_s} for s <= r, 0 above the diagonal:
+//   O   = scale [ (Q K^T . D) V + e^{G_r} Q S_in ],   S_out = e^{G_C} S_in + sum_s e^{G_C - G_s} k_s v_s^T
+// and for the gradients, with dO' = scale dO and R the gradient of S_out:
+//   dQ  = (dO' V^T . D) K    + e^{G_r} dO' S_in^T
+//   dK  = (dO' V^T . D)^T Q  + e^{G_C - G_s} V R^T
+//   dV  = (Q K^T . D)^T dO'  + e^{G_C - G_s} K R
+//   R_in = e^{G_C} R + sum_r e^{G_r} q_r dO'_r^T
+//   dg_t = sum_{r >= t > s} D_rs (q_r.k_s)(dO'_r.v_s) + sum_{r >= t} e^{G_r} q_r.(S_in dO'_r)
+//          + sum_{s < t} e^{G_C - G_s} k_s.(R v_s) + e^{G_C} <S_in, R>
+// (every term of dg is a pair of a write before t and a read from t on: nothing cancels).
+//
+// The decays are differences of cumulative sums. The sums are taken in fp64 and kept as the sum
+// of two floats, so that a difference of two nearby large values (strong decays earlier in the
+// chunk) keeps its own precision: D_rs = 2^{(hi_r - hi_s) + (lo_r - lo_s)}. A g below kMinLog2
+// in units of log2 (-infinity among them) counts as kMinLog2: 2^-200 is zero in fp32.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+struct HlaArgs {
+    const void *q = nullptr, *k = nullptr, *v = nullptr, *g = nullptr;
+    const float *S0 = nullptr;
+    void *o = nullptr;
+    float *ST = nullptr;
+    // backward
+    const void *dO = nullptr;
+    const float *dST = nullptr;
+    void *dq = nullptr, *dk_ = nullptr, *dv_ = nullptr, *dg = nullptr;  // dg null: not wanted
+    float *dS0 = nullptr;                                               // null: not wanted
+    int B = 0, T = 0, H = 0, dk = 0, dv = 0, dtype = 0;
+    int gate = 0;      // KDA_HLA_GATE_*
+    float scale = 1.f;
+    const int32_t *cu_seqlens = nullptr;
+    int N = 0;         // sequences
+    void *workspace = nullptr;
+    size_t workspace_bytes = 0;
+    int *dev_status = nullptr;
+    cudaStream_t stream = nullptr;
+};
+
+// Chunk slots. The chunk c of sequence n has a slot of its own in the workspace: n * ceil(T / C) + c
+// for dense batches, and floor(cu[n] / C) + n + c for packed ones (a sequence of len tokens has
+// ceil(len / C) <= floor(cu[n + 1] / C) - floor(cu[n] / C) + 1 chunks, so slots never meet, and no
+// prefix sum over the sequences is needed).
+inline __host__ __device__ long long hla_slots(bool packed, int N, int T, int C) {
+    return packed ? (long long)T / C + N : (long long)N * ((T + C - 1) / C);
+}
+
+struct HlaSpan {
+    long long t0;    // first token (row of the token-major tensors)
+    int len;         // tokens
+    int nch;         // chunks
+    long long slot;  // slot of chunk 0
+};
+
+// The offsets are clamped to [0, T] and to increasing order, so that no offset reaches past a tensor.
+__device__ __forceinline__ HlaSpan hla_span(const HlaArgs &p, int n, int C) {
+    HlaSpan s;
+    if (p.cu_seqlens) {
+        const int a = min(max(p.cu_seqlens[n], 0), p.T), b = min(max(p.cu_seqlens[n + 1], a), p.T);
+        s.t0 = a;
+        s.len = b - a;
+        s.slot = a / C + n;
+    } else {
+        s.t0 = (long long)n * p.T;
+        s.len = p.T;
+        s.slot = (long long)n * ((p.T + C - 1) / C);
+    }
+    s.nch = (s.len + C - 1) / C;
+    return s;
+}
+
+// Slot -> sequence and chunk; false for a slot without a chunk.
+__device__ __forceinline__ bool hla_chunk_of(const HlaArgs &p, long long slot, int C, int &n, int &c, HlaSpan &s) {
+    if (!p.cu_seqlens) {
+        const int nch = (p.T + C - 1) / C;
+        n = (int)(slot / nch);
+        c = (int)(slot - (long long)n * nch);
+        s = hla_span(p, n, C);
+        return true;
+    }
+    int lo = 0, hi = p.N - 1;  // the last sequence whose first slot is at or before this one
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int a = min(max(p.cu_seqlens[mid], 0), p.T);
+        if (a / C + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    n = lo;
+    s = hla_span(p, n, C);
+    c = (int)(slot - s.slot);
+    return c >= 0 && c < s.nch;
+}
+
+constexpr double kLog2eD = 1.4426950408889634;
+constexpr double kMinLog2 = -200.0;
+
+__device__ __forceinline__ float hla_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^(a - b) for sums kept as two floats
+__device__ __forceinline__ float hla_decay(float2 a, float2 b) { return hla_ex2((a.x - b.x) + (a.y - b.y)); }
+
+// Cumulative log2-decays of one chunk, by one warp: G[r] (r < C) as two floats each; rows from Lc on
+// decay by nothing, so that G[C - 1] is the whole chunk's. `row0` is the chunk's first token row.
+template <typename Tin, int C>
+__device__ __forceinline__ void hla_scan_gate(const HlaArgs &p, long long row0, int h, int Lc, float2 *G) {
+    constexpr int E = C / 32;
+    const int lane = threadIdx.x & 31;
+    double x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int r = lane * E + e;
+        double gv = 0.0;
+        if (r < Lc) {
+            gv = p.gate == KDA_HLA_GATE_HEAD ? (double)static_cast<const float *>(p.g)[h]
+                                             : (double)ld_elem(static_cast<const Tin *>(p.g), (size_t)(row0 + r) * p.H + h);
+            gv *= kLog2eD;
+            if (gv < kMinLog2) gv = kMinLog2;  // not fmax: a NaN stays one
+        }
+        x[e] = gv + (e ? x[e - 1] : 0.0);
+    }
+    double sum = x[E - 1];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+    }
+    double before = __shfl_up_sync(0xffffffffu, sum, 1);
+    if (lane == 0) before = 0.0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const double t = before + x[e];
+        const float hi = (float)t;
+        G[lane * E + e] = make_float2(hi, (float)(t - (double)hi));
+    }
+}
+
+// Launchers (return cudaSuccess or the launch error).
+cudaError_t launch_hla_forward_simt(const HlaArgs &a);
+size_t hla_forward_simt_workspace(const HlaArgs &a);
+cudaError_t launch_hla_backward_simt(const HlaArgs &a);
+size_t hla_backward_simt_workspace(const HlaArgs &a);
+cudaError_t launch_hla_clear_outside(const HlaArgs &a);  // packed batches: zero gradients of rows of no sequence
+
+struct HlaDecodeArgs {
+    const void *q, *k, *v, *g;
+    float *S;
+    void *o;
+    int N, H, dk, dv, dtype, gate;
+    float scale;
+    cudaStream_t stream;
+};
+cudaError_t launch_hla_decode(const HlaDecodeArgs &a);
+
+struct RopeArgs {
+    const void *q, *k;        // k may be null
+    const void *positions;    // device, int32 or int64 [B, T]; null: 0 .. T - 1 in every sequence
+    const float *inv_freq;    // device [rot_dim / 2]
+    void *q_out, *k_out;
+    long long tokens;         // B * T
+    int T, Hq, Hk, d, rot_dim;
+    bool pos64, interleaved, inverse;
+    float mscale;
+    int dtype;
+    cudaStream_t stream;
+};
+cudaError_t launch_rope(const RopeArgs &a);
+
+}  // namespace kda

@@ -10,6 +10,7 @@ pass them. There is no CPU fallback: importing this module raises if
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -76,11 +77,25 @@ _lib.kda_forward_host_varlen_workspace_size.argtypes = [_i] * 6 + [_vp, _i, _i]
 _lib.kda_forward_host_varlen_workspace_size.restype = _sz
 _lib.kda_forward_host_varlen.argtypes = [_vp] * 8 + [_i] * 6 + [_vp, _i, _i, _vp, _sz, _vp, _vp, _i]
 _lib.kda_forward_host_varlen.restype = _i
+_f = ctypes.c_float
+_lib.kda_hla_forward_workspace_size.argtypes = [_i] * 8
+_lib.kda_hla_forward_workspace_size.restype = _sz
+_lib.kda_hla_forward.argtypes = [_vp] * 7 + [_i] * 5 + [_f, _i, _i, _vp, _i, _vp, _sz, _vp, _vp, _i]
+_lib.kda_hla_forward.restype = _i
+_lib.kda_hla_backward_workspace_size.argtypes = [_i] * 8
+_lib.kda_hla_backward_workspace_size.restype = _sz
+_lib.kda_hla_backward.argtypes = [_vp] * 12 + [_i] * 5 + [_f, _i, _i, _vp, _i, _vp, _sz, _vp, _vp, _i]
+_lib.kda_hla_backward.restype = _i
+_lib.kda_hla_decode_step.argtypes = [_vp] * 6 + [_i] * 4 + [_f, _i, _i, _vp]
+_lib.kda_hla_decode_step.restype = _i
+_lib.kda_rope.argtypes = [_vp] * 3 + [_i] + [_vp] * 3 + [_i] * 8 + [_f, _i, _vp]
+_lib.kda_rope.restype = _i
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGNMENT = 0, 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_TIMEOUT, KDA_ERR_SCRATCH_LIMIT = 4, 5, 6, 7
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 PATHS = {"auto": 0, "simt": 1, "tc": 2, "tc_single": 3, "tc_split": 4, "tc_pipe": 5}
+KDA_HLA_GATE_TOKEN, KDA_HLA_GATE_HEAD = 0, 1
 KDA_FUSE_NORM_QK, KDA_FUSE_GATE_LOGITS = 1, 2  # fused pre-operations (see include/kda.h)
 
 
@@ -558,6 +573,237 @@ def kda_kcp_scan(S0, M, Z, *, stream=None):
     if rc != KDA_OK:
         raise KdaError(rc, "kda_kcp_scan")
     return S_in, S_T
+
+
+def _on(dev, stream):
+    """Device of the tensors and, when given, the call's stream made current: what is allocated inside belongs to
+    the stream that the kernels run on, so that freeing it cannot hand it to another stream's work too early."""
+    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev)
+
+
+def _hla_gate(g, dtype, shape, dev):
+    """KDA_HLA_GATE_*: g of the activations' type, one number per token and head, or fp32 ``[H]``."""
+    if isinstance(g, torch.Tensor) and g.dim() == 1:
+        _need(g, "g", torch.float32, shape[-1:], dev)
+        return KDA_HLA_GATE_HEAD
+    _need(g, "g", dtype, shape, dev)
+    return KDA_HLA_GATE_TOKEN
+
+
+def _hla_shapes(q, k, v, g, cu_seqlens):
+    _need(k, "k")
+    dtype, dev = k.dtype, k.device
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if k.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("q, k and v are [B, T, H, d]")
+    B, T, H, dk = k.shape
+    dv = v.shape[-1]
+    _need(q, "q", dtype, (B, T, H, dk), dev)
+    _need(v, "v", dtype, (B, T, H, dv), dev)
+    gate = _hla_gate(g, dtype, (B, T, H), dev)
+    N = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+        if B != 1:
+            raise ValueError("cu_seqlens needs B == 1")
+        N = cu_seqlens.numel() - 1
+    return dtype, dev, B, T, H, dk, dv, gate, N
+
+
+def _hla_workspace(size, workspace, dev, where):
+    if size == ctypes.c_size_t(-1).value:
+        raise KdaError(KDA_ERR_UNSUPPORTED, where)
+    if workspace is None:
+        return torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _need(workspace, "workspace", None, None, dev)
+    return workspace
+
+
+def kda_hla_forward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, path="auto") -> int:
+    """Bytes of workspace of kda_hla_forward (num_seqs 0: a dense batch)."""
+    n = _lib.kda_hla_forward_workspace_size(B, T, H, dk, dv, num_seqs, DTYPES.get(dtype, dtype), PATHS[path])
+    if n == ctypes.c_size_t(-1).value:
+        raise KdaError(KDA_ERR_INVALID_ARG, "kda_hla_forward_workspace_size")
+    return int(n)
+
+
+def kda_hla_backward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, path="auto") -> int:
+    """Bytes of workspace of kda_hla_backward (num_seqs 0: a dense batch)."""
+    n = _lib.kda_hla_backward_workspace_size(B, T, H, dk, dv, num_seqs, DTYPES.get(dtype, dtype), PATHS[path])
+    if n == ctypes.c_size_t(-1).value:
+        raise KdaError(KDA_ERR_INVALID_ARG, "kda_hla_backward_workspace_size")
+    return int(n)
+
+
+def kda_hla_forward(q, k, v, g, S0=None, *, scale: float = 1.0, cu_seqlens=None, o=None, S_T=None,
+                    return_state: bool = True, workspace=None, dev_status=None, stream=None, path: str = "auto"):
+    """Chunked prefill of linear attention with one decay per head: ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``,
+    ``o_t = scale S_t^T q_t``. q, k ``[B, T, H, dk]``; v ``[B, T, H, dv]`` (fp32 or bf16); g ``[B, T, H]`` of the same
+    type, or fp32 ``[H]``; S0 ``[N, H, dv, dk]`` fp32 or None; cu_seqlens int32 ``[N+1]`` (B must be 1) or None.
+    Returns ``(o, S_T)`` (S_T None when ``return_state`` is False and none is given)."""
+    dtype, dev, B, T, H, dk, dv, gate, N = _hla_shapes(q, k, v, g, cu_seqlens)
+    if S0 is not None:
+        _need(S0, "S0", torch.float32, (N, H, dv, dk), dev)
+    with _on(dev, stream), torch.cuda.device(dev):
+        if o is None:
+            # tokens outside the sequences of a packed batch are not written
+            o = torch.empty((B, T, H, dv), dtype=dtype, device=dev)
+        _need(o, "o", dtype, (B, T, H, dv), dev)
+        if return_state and S_T is None:
+            S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        if S_T is not None:
+            _need(S_T, "S_T", torch.float32, (N, H, dv, dk), dev)
+        if dev_status is not None:
+            _need(dev_status, "dev_status", torch.int32, None, dev)
+        packed = N if cu_seqlens is not None else 0
+        size = _lib.kda_hla_forward_workspace_size(B, T, H, dk, dv, packed, DTYPES[dtype], PATHS[path])
+        workspace = _hla_workspace(size, workspace, dev, "kda_hla_forward")
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = _lib.kda_hla_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(o), _ptr(S_T), B, T, H, dk, dv,
+                                  float(scale), DTYPES[dtype], gate, _ptr(cu_seqlens), packed, _ptr(workspace), ws_bytes,
+                                  _ptr(dev_status), _stream_handle(stream, dev), PATHS[path])
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_hla_forward")
+    return o, S_T
+
+
+def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, cu_seqlens=None, return_dg: bool = True,
+                     return_dS0: bool = True, workspace=None, dev_status=None, stream=None, path: str = "auto"):
+    """Gradients of kda_hla_forward's inputs from ``do`` (of o, its type and shape) and ``dS_T`` (of S_T, fp32, or
+    None: zeros). Returns ``(dq, dk, dv, dg, dS0)``; dg is None when g is ``[H]`` (a fixed number per head) or
+    ``return_dg`` is False, dS0 (fp32) is None when ``return_dS0`` is False. Rows outside the sequences of a packed
+    batch are zero."""
+    dtype, dev, B, T, H, dk, dv, gate, N = _hla_shapes(q, k, v, g, cu_seqlens)
+    _need(do, "do", dtype, (B, T, H, dv), dev)
+    for name, x in (("S0", S0), ("dS_T", dS_T)):
+        if x is not None:
+            _need(x, name, torch.float32, (N, H, dv, dk), dev)
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, None, dev)
+    with _on(dev, stream), torch.cuda.device(dev):
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dg = torch.empty_like(g) if gate == KDA_HLA_GATE_TOKEN and return_dg else None
+        dS0 = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev) if return_dS0 else None
+        packed = N if cu_seqlens is not None else 0
+        size = _lib.kda_hla_backward_workspace_size(B, T, H, dk, dv, packed, DTYPES[dtype], PATHS[path])
+        workspace = _hla_workspace(size, workspace, dev, "kda_hla_backward")
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = _lib.kda_hla_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(do), _ptr(dS_T), _ptr(dq), _ptr(dk_),
+                                   _ptr(dv_), _ptr(dg), _ptr(dS0), B, T, H, dk, dv, float(scale), DTYPES[dtype], gate,
+                                   _ptr(cu_seqlens), packed, _ptr(workspace), ws_bytes, _ptr(dev_status),
+                                   _stream_handle(stream, dev), PATHS[path])
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_hla_backward")
+    return dq, dk_, dv_, dg, dS0
+
+
+def kda_hla_decode_step(q, k, v, g, S, o=None, *, scale: float = 1.0, stream=None):
+    """One token of the same recurrence per request. q, k ``[N, H, dk]``; v ``[N, H, dv]``; g ``[N, H]`` of the same
+    type or fp32 ``[H]``; S ``[N, H, dv, dk]`` fp32 updated in place. Returns o."""
+    _need(k, "k")
+    dtype, dev = k.dtype, k.device
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if k.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("q, k and v are [N, H, d]")
+    N, H, dk = k.shape
+    dv = v.shape[-1]
+    _need(q, "q", dtype, (N, H, dk), dev)
+    _need(v, "v", dtype, (N, H, dv), dev)
+    gate = _hla_gate(g, dtype, (N, H), dev)
+    _need(S, "S", torch.float32, (N, H, dv, dk), dev)
+    with _on(dev, stream), torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty((N, H, dv), dtype=dtype, device=dev)
+        _need(o, "o", dtype, (N, H, dv), dev)
+        rc = _lib.kda_hla_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(o), N, H, dk, dv, float(scale),
+                                      DTYPES[dtype], gate, _stream_handle(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_hla_decode_step")
+    return o
+
+
+def kda_rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                      original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Frequencies and magnitude of kda_rope for contexts ``factor`` times the trained length. Returns
+    ``(inv_freq, mscale)``: fp32 ``[rot_dim / 2]`` and a number. ``scaling``:
+
+    - ``"none"``: base^(-2 i / rot_dim), mscale 1;
+    - ``"linear"``: those divided by factor (positions interpolated);
+    - ``"base"``: the base times factor^(rot_dim / (rot_dim - 2)), which divides the slowest pair's frequency by factor
+      and leaves the fastest as it is;
+    - ``"ramp"``: pairs that turn more than beta_fast times over original_length keep their frequency, those that turn
+      less than beta_slow times are divided by factor, with a linear ramp over the pairs' index between, and mscale
+      0.1 ln(factor) + 1."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    if not factor >= 1.0 or not base > 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "base":
+        if rot_dim == 2:
+            raise ValueError("the base of a single pair cannot be scaled")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    inv = base ** (-i / rot_dim)
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "ramp":
+        if original_length <= 0 or not beta_fast > beta_slow > 0:
+            raise ValueError("ramp scaling needs original_length and beta_fast > beta_slow > 0")
+        # the (fractional) index of the pair that turns b times over the original length
+        at = [rot_dim * math.log(original_length / (2 * math.pi * b)) / (2 * math.log(base)) for b in (beta_fast, beta_slow)]
+        lo, hi = max(0.0, math.floor(at[0])), min(rot_dim - 1.0, math.ceil(at[1]))
+        keep = 1.0 - ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        inv = inv / factor * (1.0 - keep) + inv * keep
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return inv.to(torch.float32).to(device if device is not None else "cpu"), mscale
+
+
+def kda_rope(q, k, inv_freq, *, positions=None, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
+             q_out=None, k_out=None, stream=None):
+    """Rotary positions of q ``[B, T, Hq, d]`` and k ``[B, T, Hk, d]`` (or None), over the first ``2 * len(inv_freq)``
+    channels: pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when ``interleaved``. inv_freq: fp32 on the device
+    (kda_rope_inv_freq); positions: int32 or int64 ``[B, T]`` or None (0 .. T - 1). ``inverse`` turns back: with the same
+    mscale it takes the outputs' gradients to the inputs'. ``q_out`` / ``k_out`` may be q and k (in place). Returns
+    ``(q_out, k_out)``."""
+    _need(q, "q")
+    dtype, dev = q.dtype, q.device
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if q.dim() != 4:
+        raise ValueError("q is [B, T, H, d]")
+    B, T, Hq, d = q.shape
+    Hk = 0
+    if k is not None:
+        _need(k, "k", dtype, None, dev)
+        if k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != d:
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected {(B, T, 'Hk', d)}")
+        Hk = k.shape[2]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _need(inv_freq, "inv_freq", torch.float32, None, dev)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq is [rot_dim / 2]")
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"positions has dtype {positions.dtype}, expected int32 or int64")
+        _need(positions, "positions", None, (B, T), dev)
+    with _on(dev, stream), torch.cuda.device(dev):
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        _need(q_out, "q_out", dtype, q.shape, dev)
+        if k is not None:
+            k_out = torch.empty_like(k) if k_out is None else k_out
+            _need(k_out, "k_out", dtype, k.shape, dev)
+        rc = _lib.kda_rope(_ptr(q), _ptr(k), _ptr(positions), int(positions is not None and positions.dtype == torch.int64),
+                           _ptr(inv_freq), _ptr(q_out), _ptr(k_out), B, T, Hq, Hk, d, 2 * inv_freq.numel(),
+                           int(interleaved), int(inverse), float(mscale), DTYPES[dtype], _stream_handle(stream, dev))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_rope")
+    return q_out, k_out
 
 
 def kda_selftest_wait_timeout(dev_status, max_cycles: int = 20_000_000, *, stream=None):
