@@ -473,9 +473,13 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
  *            time.
  *   dev_status : NULL, or a device int set to KDA_ERR_TIMEOUT if a bounded
  *            wait of a tensor-core kernel gives up.
- *   path   : KDA_PATH_AUTO or KDA_PATH_SIMT (kda_path).
+ *   path   : KDA_PATH_AUTO, KDA_PATH_SIMT (CUDA cores) or KDA_PATH_TC (tensor
+ *            cores; bf16 only, else KDA_ERR_UNSUPPORTED). AUTO takes the tensor
+ *            cores for bf16.
  *
- * Arithmetic: sums, states and decays in fp32 (the decays' sums in fp64).
+ * Arithmetic: sums, states and decays in fp32 (the decays' sums in fp64). The
+ * tensor cores take the scores and the states as bf16 operands; the states
+ * themselves are carried in fp32, to about 2^-18.
  *
  * kda_hla_backward: the gradients of q, k, v, g and S0 from dO, the outputs'
  * (dtype, [B, T, H, dv]), and dS_T, the last states' (fp32, or NULL: zeros).

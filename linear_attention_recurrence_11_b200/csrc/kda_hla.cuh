@@ -151,6 +151,11 @@ size_t hla_forward_simt_workspace(const HlaArgs &a);
 cudaError_t launch_hla_backward_simt(const HlaArgs &a);
 size_t hla_backward_simt_workspace(const HlaArgs &a);
 cudaError_t launch_hla_clear_outside(const HlaArgs &a);  // packed batches: zero gradients of rows of no sequence
+// the tensor-core kernels: bf16, every head size
+bool hla_tc_supported(const HlaArgs &a);
+size_t hla_tc_workspace(const HlaArgs &a, bool back);
+cudaError_t launch_hla_forward_tc(const HlaArgs &a);
+cudaError_t launch_hla_backward_tc(const HlaArgs &a);
 
 struct HlaDecodeArgs {
     const void *q, *k, *v, *g;

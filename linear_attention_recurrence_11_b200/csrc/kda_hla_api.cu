@@ -11,22 +11,32 @@ bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool dtype_ok(int t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_BF16; }
 bool gate_ok(int g) { return g == KDA_HLA_GATE_TOKEN || g == KDA_HLA_GATE_HEAD; }
 
+// Marks a packed batch in size queries (compared against null, never dereferenced).
+const int32_t kPackedMarker = 0;
+
 // Validates the shape arguments shared by the prefill and its backward pass; fills the sizes.
 int check_sizes(int B, int T, int H, int dk, int dv, int dtype, bool packed, int num_seqs, int path, kda::HlaArgs *a) {
     if (B <= 0 || T < 0 || H <= 0 || !dtype_ok(dtype)) return KDA_ERR_INVALID_ARG;
     if (packed && (B != 1 || num_seqs <= 0)) return KDA_ERR_INVALID_ARG;
-    if (path != KDA_PATH_AUTO && path != KDA_PATH_SIMT) return KDA_ERR_INVALID_ARG;
+    if (path != KDA_PATH_AUTO && path != KDA_PATH_SIMT && path != KDA_PATH_TC) return KDA_ERR_INVALID_ARG;
     if (!head_dim_ok(dk) || !head_dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
     a->B = B; a->T = T; a->H = H; a->dk = dk; a->dv = dv; a->dtype = dtype;
     a->N = packed ? num_seqs : B;
     // one block per (sequence, head) and per (chunk slot, head), in 31-bit grids
     if ((long long)a->N * H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     if (kda::hla_slots(packed, a->N, T, 64) > 0x7fffffffLL / H) return KDA_ERR_UNSUPPORTED;
+    a->cu_seqlens = packed ? &kPackedMarker : nullptr;
+    if (path == KDA_PATH_TC && !kda::hla_tc_supported(*a)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
-// Marks a packed batch in size queries (compared against null, never dereferenced).
-const int32_t kPackedMarker = 0;
+// The tensor cores take every bf16 call that has tokens; a batch without any only hands its states on.
+bool use_tc(const kda::HlaArgs &a, int path) { return path != KDA_PATH_SIMT && a.T > 0 && kda::hla_tc_supported(a); }
+
+size_t workspace_of(const kda::HlaArgs &a, bool back, int path) {
+    if (use_tc(a, path)) return kda::hla_tc_workspace(a, back);
+    return back ? kda::hla_backward_simt_workspace(a) : kda::hla_forward_simt_workspace(a);
+}
 
 }  // namespace
 
@@ -35,15 +45,13 @@ extern "C" {
 size_t kda_hla_forward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype, int path) {
     kda::HlaArgs a{};
     if (num_seqs < 0 || check_sizes(B, T, H, dk, dv, dtype, num_seqs > 0, num_seqs, path, &a)) return (size_t)-1;
-    a.cu_seqlens = num_seqs > 0 ? &kPackedMarker : nullptr;
-    return kda::hla_forward_simt_workspace(a);
+    return workspace_of(a, false, path);
 }
 
 size_t kda_hla_backward_workspace_size(int B, int T, int H, int dk, int dv, int num_seqs, int dtype, int path) {
     kda::HlaArgs a{};
     if (num_seqs < 0 || check_sizes(B, T, H, dk, dv, dtype, num_seqs > 0, num_seqs, path, &a)) return (size_t)-1;
-    a.cu_seqlens = num_seqs > 0 ? &kPackedMarker : nullptr;
-    return kda::hla_backward_simt_workspace(a);
+    return workspace_of(a, true, path);
 }
 
 int kda_hla_forward(const void *q, const void *k, const void *v, const void *g, const float *S0, void *o, float *S_T,
@@ -61,9 +69,9 @@ int kda_hla_forward(const void *q, const void *k, const void *v, const void *g, 
     a.scale = scale; a.gate = gate; a.cu_seqlens = cu_seqlens;
     a.workspace = workspace; a.workspace_bytes = workspace_bytes; a.dev_status = dev_status;
     a.stream = static_cast<cudaStream_t>(stream);
-    const size_t need = kda::hla_forward_simt_workspace(a);
+    const size_t need = workspace_of(a, false, path);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
-    return kda::cuda_status(kda::launch_hla_forward_simt(a));
+    return kda::cuda_status(use_tc(a, path) ? kda::launch_hla_forward_tc(a) : kda::launch_hla_forward_simt(a));
 }
 
 int kda_hla_backward(const void *q, const void *k, const void *v, const void *g, const float *S0, const void *dO,
@@ -85,13 +93,13 @@ int kda_hla_backward(const void *q, const void *k, const void *v, const void *g,
     a.scale = scale; a.gate = gate; a.cu_seqlens = cu_seqlens;
     a.workspace = workspace; a.workspace_bytes = workspace_bytes; a.dev_status = dev_status;
     a.stream = static_cast<cudaStream_t>(stream);
-    const size_t need = kda::hla_backward_simt_workspace(a);
+    const size_t need = workspace_of(a, true, path);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (cu_seqlens && T > 0) {
         const cudaError_t e = kda::launch_hla_clear_outside(a);
         if (e != cudaSuccess) return kda::cuda_status(e);
     }
-    return kda::cuda_status(kda::launch_hla_backward_simt(a));
+    return kda::cuda_status(use_tc(a, path) ? kda::launch_hla_backward_tc(a) : kda::launch_hla_backward_simt(a));
 }
 
 int kda_hla_decode_step(const void *q, const void *k, const void *v, const void *g, float *S, void *o, int N, int H,

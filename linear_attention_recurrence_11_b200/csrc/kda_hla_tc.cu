@@ -1,0 +1,724 @@
+// Linear attention with one decay per head on the 5th-generation tensor cores (bf16 inputs, fp32
+// states, every head size; 32 channels are padded to 64 by the copies' zero fill): prefill and its
+// backward pass, in chunks of 128 tokens. The chunked form is in kda_hla.cuh.
+//
+// Two steps. The state kernel carries the state (and, for the backward pass, its gradient from the
+// last chunk to the first) over the chunks and leaves each chunk's incoming one in the workspace as a
+// bf16 operand tile. The tile kernels then take every (chunk, head) on its own: with X, Y, Z tiles of
+// the chunk and W a state,
+//     out = c1 (X Y^T . D) Z + c2 X W,       c2 per row,
+// which is the output (X, Y, Z, W = Q, K, V, S) and each of the gradients dQ (dO, V, K, S),
+// dK (V, dO, Q, R) and dV (K, Q, dO, R), the last two with D transposed.
+//
+// Roundings to bf16: the masked scores (as the operand of the second product), the states (as an
+// operand; they are carried in fp32), and the results. The state's own update multiplies k v^T by a
+// decay per token; that product is taken as the sum of two bf16 numbers (hi + lo, 16 bits of the 24),
+// so that the fp32 state is good to about 2^-18 and not to 2^-9.
+#include "kda_hla.cuh"
+#include "kda_sm100.cuh"
+#include "kda_tc_common.cuh"
+
+namespace kda {
+namespace {
+
+using namespace sm100;
+using tc::kWaitCycles;
+using tc::mma_chain;
+using tc::Opnd;
+using tc::pack_bf2;
+
+constexpr int C = 128;               // tokens per chunk
+constexpr uint32_t KB = 1024;
+constexpr uint32_t TILE = 16 * KB;   // 128 rows of 64 bf16 (128-byte swizzled rows)
+
+__host__ __device__ constexpr int padded(int d) { return d < 64 ? 64 : d; }
+
+// Bytes of one chunk's state operand: [dk / 64][dv rows][64 dk] bf16, swizzled as in shared memory.
+__host__ __device__ inline size_t blob_bytes(int dkp, int dvp) { return (size_t)dkp * dvp * 2; }
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// ================================================================= states
+// Direction 0: the state; a = k, b = v, row weights e^{G_C - G_s}, chunks in order, from S0 to S_T.
+// Direction 1: its gradient; a = q, b = dO, row weights scale e^{G_r}, chunks from the last to the
+// first, from dS_T to dS0. Per chunk X <- e^{G_C} X + b^T (w a), X [dv][dk].
+struct StateArgs {
+    HlaArgs a;
+    uint8_t *blob[2];   // per direction: chunk operands [slot][H]
+    float *seg[2];      // per direction: states of the segments [segment slot][H][dv][dk]
+    float *seg_keep[2]; // per direction: decay over each segment [segment slot][H]
+    int sc;             // chunks per segment; 0: whole sequences
+    bool ends;          // first pass over segments: from zero, only the end states
+};
+
+// One CTA: all dv rows (the MMA's M) and 64 columns of dk. Thread: one row of X (a TMEM lane), whose
+// 64 columns it holds in registers; as a token it scales one row of a.
+template <int DVP>
+struct StateSmem {
+    static constexpr uint32_t B = 0, A = (DVP / 64) * TILE, LO = A + TILE, MISC = LO + TILE;
+    static constexpr uint32_t G = MISC + 64;                  // 2 x 128 float2
+    static constexpr uint32_t bytes = G + 2 * C * 8 + 1024;   // slack for 1024-byte alignment
+};
+
+template <int DKP, int DVP>
+__global__ void __launch_bounds__(128) hla_state_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
+                                                           const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
+                                                           const StateArgs s, int dir0) {
+    using L = StateSmem<DVP>;
+    const HlaArgs &p = s.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(sm);
+    uint64_t *bar_tma = reinterpret_cast<uint64_t *>(sm + L::MISC), *bar_mma = bar_tma + 1;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bar_tma + 2);
+    float2 *G = reinterpret_cast<float2 *>(sm + L::G);
+
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int dir = blockIdx.z + dir0, slice = blockIdx.y;
+    const int h = blockIdx.x % p.H;
+    const long long su = blockIdx.x / p.H;  // sequence, or segment slot
+    int n = (int)su, sg = 0;
+    HlaSpan sp;
+    if (s.sc) {
+        hla_chunk_of(p, su, s.sc * C, n, sg, sp);
+        if (sg < 0 || sg >= max(1, sp.nch)) return;  // (an empty sequence keeps one segment, which passes its state on)
+    }
+    sp = hla_span(p, n, C);
+    const int nseg = s.sc ? max(1, (sp.nch + s.sc - 1) / s.sc) : 1;
+    const int c0 = s.sc ? sg * s.sc : 0, c1 = s.sc ? min(sp.nch, c0 + s.sc) : sp.nch;
+    const bool last = dir ? sg == 0 : sg == nseg - 1;  // the segment whose end is the sequence's
+    if (s.ends && last) return;
+    const size_t sbase_n = ((size_t)n * p.H + h) * (size_t)(p.dv * p.dk), sbase_s = ((size_t)su * p.H + h) * (size_t)(p.dv * p.dk);
+    const float *start = s.ends ? nullptr : s.sc ? s.seg[dir] + sbase_s : dir ? p.dST : p.S0;
+    if (start && !s.sc) start += sbase_n;
+    float *end = s.ends ? s.seg[dir] + sbase_s : (!last ? nullptr : dir ? p.dS0 : p.ST);
+    if (end && !s.ends) end += sbase_n;
+
+    const int row = tid, cols = min(64, p.dk - 64 * slice);  // this thread's row of X, and the columns that exist
+    const size_t row_off = (size_t)row * p.dk + 64 * slice;
+    float x[64];
+#pragma unroll
+    for (int e = 0; e < 64; e += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (start && row < p.dv && e < cols) v = *reinterpret_cast<const float4 *>(start + row_off + e);
+        x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
+    }
+
+    if (tid == 0) {
+        mbar_init(bar_tma, 1);
+        mbar_init(bar_mma, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(s_tmem, 64);
+        tmem_relinquish();
+    }
+    const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
+    const auto scan = [&](int i) {
+        const int c = chunk(i);
+        hla_scan_gate<__nv_bfloat16, C>(p, sp.t0 + (long long)c * C, h, min(C, sp.len - c * C), G + (i & 1) * C);
+    };
+    if (c0 < c1 && warp == 1) scan(0);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t tlane = (uint32_t)(32 * warp) << 16;
+
+    const auto issue = [&](int i) {  // one thread: the tiles of chunk i
+        const int tok = (int)(sp.t0 + (long long)chunk(i) * C);
+        mbar_arrive_expect_tx(bar_tma, (1 + DVP / 64) * TILE);
+        tma_load_3d(sm + L::A, dir ? &tm_a1 : &tm_a0, bar_tma, 64 * slice, h, tok);
+#pragma unroll
+        for (int b = 0; b < DVP / 64; ++b) tma_load_3d(sm + L::B + b * TILE, dir ? &tm_b1 : &tm_b0, bar_tma, 64 * b, h, tok);
+    };
+    const int nc = c1 - c0;
+    if (tid == 0 && nc > 0) issue(0);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 64, 1, 1);
+    uint32_t ph = 0;
+    bool aborted = false, tma_open = nc > 0, mma_open = false;
+    float total = 1.f;  // decay over the segment
+    for (int i = 0; i < nc; ++i) {
+        const int c = chunk(i), Lc = min(C, sp.len - c * C);
+        const bool more = i + 1 < nc;
+        const float2 g0 = make_float2(0.f, 0.f), gC = G[(i & 1) * C + C - 1], gt = G[(i & 1) * C + tid];
+        const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(gC, gt), keep = hla_decay(gC, g0);
+        total *= keep;
+        const bool ok_t = mbar_wait_bounded(bar_tma, ph, kWaitCycles);
+        tma_open = !ok_t;
+        // row `tid` of a, times its weight, as hi + lo; a row behind the sequence's end is zero on both
+        // sides of the product (what stands there may be anything)
+        uint8_t *ra = sm + L::A, *rl = sm + L::LO;
+        if (tid < Lc) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t off = sw128_offset(tid, 8 * q);
+                const uint4 v = *reinterpret_cast<const uint4 *>(ra + off);
+                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = w * bf_lo(in[e]), b = w * bf_hi(in[e]);
+                    hi[e] = pack_bf2(a, b);
+                    lo[e] = pack_bf2(a - bf_lo(hi[e]), b - bf_hi(hi[e]));
+                }
+                *reinterpret_cast<uint4 *>(ra + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(rl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        } else {
+            const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t off = sw128_offset(tid, 8 * q);
+                *reinterpret_cast<uint4 *>(ra + off) = z;
+                *reinterpret_cast<uint4 *>(rl + off) = z;
+#pragma unroll
+                for (int b = 0; b < DVP / 64; ++b) *reinterpret_cast<uint4 *>(sm + L::B + b * TILE + off) = z;
+            }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if (__syncthreads_or(!ok_t)) { aborted = true; break; }
+        if (tid == 0) {  // (a 64-row dv is read twice as the upper half of M: lanes that nothing reads)
+            tc_fence_after();
+            const Opnd Ab{sbase + L::B, true, 0, DVP == 128 ? TILE : 0u};
+            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::A, true, 0, 0}, idesc, false);
+            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::LO, true, 0, 0}, idesc, true);
+            mma_commit(bar_mma);
+        }
+        if (!s.ends && row < DVP) {  // the state that this chunk starts from
+            uint8_t *dst = s.blob[dir] + ((size_t)(sp.slot + c) * p.H + h) * blob_bytes(DKP, DVP) + (size_t)slice * DVP * 128;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * q)) =
+                    make_uint4(pack_bf2(x[8 * q], x[8 * q + 1]), pack_bf2(x[8 * q + 2], x[8 * q + 3]),
+                               pack_bf2(x[8 * q + 4], x[8 * q + 5]), pack_bf2(x[8 * q + 6], x[8 * q + 7]));
+        }
+        if (more && warp == 1) scan(i + 1);
+        const bool ok_m = mbar_wait_bounded(bar_mma, ph, kWaitCycles);
+        mma_open = !ok_m;
+        ph ^= 1u;
+        tc_fence_after();
+        if (ok_m) {
+            if (more && tid == 0) {
+                issue(i + 1);
+                tma_open = true;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float d[16];
+                tmem_ld16(tmem + tlane + 16u * q, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[16 * q + e] = fmaf(keep, x[16 * q + e], d[e]);
+            }
+        }
+        tc_fence_before();
+        if (__syncthreads_or(!ok_m)) { aborted = true; break; }
+    }
+    if (aborted) {  // leave nothing in flight behind (the waits are bounded again)
+        if (tid == 0) {
+            if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
+            // a copy that is open was issued for the phase after the one that the MMA wait flipped to
+            if (tma_open) mbar_wait_bounded(bar_tma, ph, kWaitCycles);
+            if (mma_open) mbar_wait_bounded(bar_mma, ph ^ 1u, kWaitCycles);
+        }
+    } else if (end && row < p.dv) {
+#pragma unroll
+        for (int e = 0; e < 64; e += 4)
+            if (e < cols) *reinterpret_cast<float4 *>(end + row_off + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        if (s.ends && tid == 0 && slice == 0) s.seg_keep[dir][su * p.H + h] = total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 64);
+    }
+}
+
+// End states of the segments -> their start states: start_0 = S0, start_{i+1} = keep_i start_i + end_i (in the
+// direction's order), in place, one thread per four elements of a (sequence, head).
+__global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s, int dir0) {
+    const HlaArgs &p = s.a;
+    const int dir = blockIdx.z + dir0, h = blockIdx.x % p.H, n = blockIdx.x / p.H;
+    const int at = 4 * (blockIdx.y * 256 + threadIdx.x), size = p.dv * p.dk;
+    if (at >= size) return;
+    const HlaSpan sp = hla_span(p, n, s.sc * C);
+    const int nseg = max(1, sp.nch);
+    const float *first = dir ? p.dST : p.S0;
+    float4 x = first ? *reinterpret_cast<const float4 *>(first + ((size_t)n * p.H + h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto where = [&](int i) { return (size_t)(sp.slot + (dir ? nseg - 1 - i : i)) * p.H + h; };
+    for (int i = 0; i < nseg; ++i) {
+        float4 *y = reinterpret_cast<float4 *>(s.seg[dir] + where(i) * size + at);
+        float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+        float keep = 0.f;
+        if (i + 1 < nseg) {
+            e = *y;
+            keep = s.seg_keep[dir][where(i)];
+        }
+        *y = x;
+        x = make_float4(fmaf(keep, x.x, e.x), fmaf(keep, x.y, e.y), fmaf(keep, x.z, e.z), fmaf(keep, x.w, e.w));
+    }
+}
+
+// ================================================================== tiles
+struct TileArgs {
+    HlaArgs a;
+    const uint8_t *S, *R;   // the chunks' states and their gradients
+    float *dots;            // [slot][H][parts][2][128]: partial row sums for dg (null: not wanted)
+    float *through;         // [slot][H][dk slices]
+};
+
+// Shared memory of a tile: X, Y (XD channels), Z (64 channels), W (64 columns of the result), the
+// scores (over Y where that has room), and G.
+template <int XD>
+struct TileSmem {
+    static constexpr uint32_t X = 0, Y = (XD / 64) * TILE, P = XD == 128 ? Y : Y + TILE;
+    static constexpr uint32_t Z = P + 2 * TILE, W = Z + TILE, MISC = W + (XD / 64) * 8 * KB;
+    static constexpr uint32_t G = MISC + 64, RED = G + C * 8;   // RED: 2 x 128 float2, and 8 floats
+    static constexpr uint32_t bytes = RED + 2 * C * 8 + 64 + 1024;
+};
+
+// kKMajor: the state's rows (dv) are the result's columns (outputs, dV); else its dk are (dQ, dK).
+// kLower: D_rs for s <= r, and c2 = scale e^{G_r}; else D_sr for s >= r, and c2 = e^{G_C - G_r}.
+// z: 64-column slice of the result.
+template <int XD, int DKP, int DVP, bool kKMajor, bool kLower, bool kDots>
+__device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUtensorMap *tmY, const CUtensorMap *tmZ, const uint8_t *blobs,
+                          const float *border, void *out, int out_d, const void *dot_src, long long slot, int h, int z, int part,
+                          int parts) {
+    using L = TileSmem<XD>;
+    const HlaArgs &p = t.a;
+    int n, c;
+    HlaSpan sp;
+    if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(sm);
+    uint64_t *bar_xy = reinterpret_cast<uint64_t *>(sm + L::MISC), *bar_zw = bar_xy + 1, *bar_s = bar_xy + 2, *bar_o = bar_xy + 3;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bar_xy + 4);
+    float2 *G = reinterpret_cast<float2 *>(sm + L::G);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, half = warp >> 2;
+    const long long row0 = sp.t0 + (long long)c * C;
+    const int Lc = min(C, sp.len - c * C);
+    const bool has = border != nullptr || (kLower ? c > 0 : c + 1 < sp.nch);  // a state that is not all zeros
+    constexpr uint32_t WB = (XD / 64) * 8 * KB;  // the state's slice: 64 rows of XD, or XD rows of 64
+
+    if (tid == 0) {
+        mbar_init(bar_xy, 1);
+        mbar_init(bar_zw, 1);
+        mbar_init(bar_s, 1);
+        mbar_init(bar_o, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(bar_xy, 2 * (XD / 64) * TILE);
+#pragma unroll
+        for (int b = 0; b < XD / 64; ++b) {
+            tma_load_3d(sm + L::X + b * TILE, tmX, bar_xy, 64 * b, h, (int)row0);
+            tma_load_3d(sm + L::Y + b * TILE, tmY, bar_xy, 64 * b, h, (int)row0);
+        }
+        mbar_arrive_expect_tx(bar_zw, TILE + (has ? WB : 0u));
+        tma_load_3d(sm + L::Z, tmZ, bar_zw, 64 * z, h, (int)row0);
+        if (has) {
+            const uint8_t *src = blobs + ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP);
+            if (kKMajor) {  // rows 64 z .. + 63 of every block of 64 dk
+#pragma unroll
+                for (int b = 0; b < XD / 64; ++b)
+                    bulk_load(sm + L::W + b * 8 * KB, src + (size_t)b * DVP * 128 + (size_t)z * 8 * KB, 8 * KB, bar_zw);
+            } else {        // block z of dk: all dv rows
+                bulk_load(sm + L::W, src + (size_t)z * DVP * 128, WB, bar_zw);
+            }
+        }
+    }
+    if (warp == 0) {
+        __syncwarp();
+        tmem_alloc(s_tmem, 256);
+        tmem_relinquish();
+    }
+    if (warp == 1) hla_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem, tlane = (uint32_t)(32 * quarter) << 16;
+    constexpr uint32_t TS = 0, T1 = 128, T2 = 192;  // scores, (scores) Z, X W
+
+    bool ok = true;
+    if (tid == 0) {
+        ok = mbar_wait_bounded(bar_xy, 0, kWaitCycles);
+        if (ok) {
+            mma_chain<XD / 16>(tmem + TS, Opnd{sbase + L::X, false, TILE, 0}, Opnd{sbase + L::Y, false, TILE, 0},
+                               idesc_bf16_f32(128, 128, 0, 0), false);
+            mma_commit(bar_s);
+        }
+    }
+    __syncwarp();
+    const bool ok_zw = mbar_wait_bounded(bar_zw, 0, kWaitCycles);
+    if (tid == 0 && ok && ok_zw && has)
+        mma_chain<XD / 16>(tmem + T2, Opnd{sbase + L::X, false, TILE, 0},
+                           Opnd{sbase + L::W, !kKMajor, 8 * KB, 0}, idesc_bf16_f32(128, 64, 0, kKMajor ? 0 : 1), false);
+    if (Lc < C && ok_zw) {  // rows of Z behind the sequence's end: zero, whatever stands there
+        for (int i = tid; i < (C - Lc) * 8; i += 256)
+            *reinterpret_cast<uint4 *>(sm + L::Z + sw128_offset(Lc + (i >> 3), 8 * (i & 7))) = make_uint4(0, 0, 0, 0);
+    }
+    float thr = 0.f;
+    if (kDots && !kLower && t.dots && ok_zw && has && (c > 0 || p.S0)) {  // <S, R> over this slice
+        const uint8_t *S = t.S + ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP) + (size_t)z * DVP * 128;
+#pragma unroll
+        for (int i = 0; i < (int)(WB / 16 / 256); ++i) {
+            const uint32_t off = 16u * (tid + 256 * i);
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(S + off)), b = *reinterpret_cast<const uint4 *>(sm + L::W + off);
+            thr = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), thr));
+            thr = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), thr));
+            thr = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), thr));
+            thr = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), thr));
+        }
+    }
+    __syncwarp();
+    const bool ok_s = mbar_wait_bounded(bar_s, 0, kWaitCycles);
+    tc_fence_after();
+
+    // scores -> decayed, masked, bf16: the K-major operand of the second product
+    const int r = 32 * quarter + lane;
+    const float2 gr = G[r];
+    if (ok_s) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int s0 = 64 * half + 16 * q;
+            uint32_t w[8];
+            // a block of 32 rows and 16 columns that the mask leaves nothing of is not computed
+            const bool none = kLower ? s0 > 32 * quarter + 31 : s0 + 15 < 32 * quarter;
+            if (none) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = 0u;
+            } else {
+                float v[16];
+                tmem_ld16(tmem + tlane + TS + s0, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int s = s0 + e;
+                    const float2 gs = G[s];
+                    const float d = kLower ? hla_decay(gr, gs) : hla_decay(gs, gr);
+                    v[e] = (kLower ? s <= r : s >= r && s < Lc) ? v[e] * d : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = pack_bf2(v[2 * e], v[2 * e + 1]);
+            }
+            uint8_t *dst = sm + L::P + half * TILE;
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 16 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 16 * q + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    const bool bad = __syncthreads_or(!ok || !ok_zw || !ok_s);
+    bool ok_o = false;
+    if (!bad) {
+        if (tid == 0) {
+            tc_fence_after();
+            mma_chain<C / 16>(tmem + T1, Opnd{sbase + L::P, false, TILE, 0}, Opnd{sbase + L::Z, true, 0, 0},
+                              idesc_bf16_f32(128, 64, 0, 1), false);
+            mma_commit(bar_o);
+        }
+        __syncwarp();
+        ok_o = mbar_wait_bounded(bar_o, 0, kWaitCycles);
+        tc_fence_after();
+    }
+    if (ok_o) {
+        const float2 g0 = make_float2(0.f, 0.f);
+        const float c2 = kLower ? p.scale * hla_decay(gr, g0) : hla_decay(G[C - 1], gr);
+        const int col = 64 * z + 32 * half;
+        const bool live = r < Lc && col < out_d;
+        const size_t at = ((size_t)(row0 + r) * p.H + h) * out_d + col;
+        float d1 = 0.f, d2 = 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float v1[16], v2[16];
+            tmem_ld16(tmem + tlane + T1 + 32u * half + 16u * q, v1);
+            if (has) tmem_ld16(tmem + tlane + T2 + 32u * half + 16u * q, v2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                v1[e] *= p.scale;
+                v2[e] = has ? v2[e] * c2 : 0.f;
+            }
+            if (live) {
+                if (kDots && t.dots) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(dot_src) + at + 16 * q);
+                    const uint4 a = __ldg(src), b = __ldg(src + 1);
+                    const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        d1 = fmaf(v1[2 * e], bf_lo(in[e]), fmaf(v1[2 * e + 1], bf_hi(in[e]), d1));
+                        d2 = fmaf(v2[2 * e], bf_lo(in[e]), fmaf(v2[2 * e + 1], bf_hi(in[e]), d2));
+                    }
+                }
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = pack_bf2(v1[2 * e] + v2[2 * e], v1[2 * e + 1] + v2[2 * e + 1]);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at + 16 * q);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+        if (kDots && t.dots) {
+            float2 *red = reinterpret_cast<float2 *>(sm + L::RED);
+            red[half * C + r] = make_float2(d1, d2);
+            if (!kLower) {
+#pragma unroll
+                for (int off = 16; off; off >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, off);
+                if (lane == 0) reinterpret_cast<float *>(red + 2 * C)[warp] = thr;
+            }
+        }
+    }
+    tc_fence_before();
+    const bool failed = __syncthreads_or(!ok_o);
+    if (kDots && t.dots && !failed) {
+        const float2 *red = reinterpret_cast<const float2 *>(sm + L::RED);
+        float *dst = t.dots + (((size_t)slot * p.H + h) * parts + part) * (2 * C);
+        if (tid < C) {
+            dst[tid] = red[tid].x + red[C + tid].x;
+            dst[C + tid] = red[tid].y + red[C + tid].y;
+        }
+        if (!kLower && tid == 0) {
+            float u = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u += reinterpret_cast<const float *>(red + 2 * C)[i];
+            t.through[((size_t)slot * p.H + h) * (DKP / 64) + z] = hla_decay(G[C - 1], make_float2(0.f, 0.f)) * u;
+        }
+    }
+    if (failed && tid == 0) {  // leave nothing in flight behind
+        if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
+        mbar_wait_bounded(bar_xy, 0, kWaitCycles);
+        mbar_wait_bounded(bar_zw, 0, kWaitCycles);
+        mma_commit(bad ? bar_o : bar_s);  // whatever products were issued (bar_s and bar_o count one arrival each)
+        mbar_wait_bounded(bad ? bar_o : bar_s, bad ? 0u : 1u, kWaitCycles);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+template <int DKP, int DVP>
+__global__ void __launch_bounds__(256, 2) hla_out_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                                                            const __grid_constant__ CUtensorMap tm_v, const TileArgs t) {
+    constexpr int parts = DVP / 64;
+    const int z = blockIdx.x % parts;
+    const unsigned u = blockIdx.x / parts;
+    tile_body<DKP, DKP, DVP, true, true, false>(t, &tm_q, &tm_k, &tm_v, t.S, t.a.S0, t.a.o, t.a.dv, nullptr, u / t.a.H, u % t.a.H, z, 0, 1);
+}
+
+// The slices of dQ, dK and dV of a (chunk, head) are neighbours in the grid: they read the same tiles, from L2.
+template <int DKP, int DVP>
+__global__ void __launch_bounds__(256, 2) hla_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                                                             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                                                             const TileArgs t) {
+    constexpr int KS = DKP / 64, VS = DVP / 64, parts = 2 * KS + VS;
+    const HlaArgs &p = t.a;
+    const int part = blockIdx.x % parts;
+    const unsigned u = blockIdx.x / parts;
+    const long long slot = u / p.H;
+    const int h = u % p.H;
+    if (part < KS)
+        tile_body<DVP, DKP, DVP, false, true, true>(t, &tm_o, &tm_v, &tm_k, t.S, p.S0, p.dq, p.dk, p.q, slot, h, part, part, 2 * KS);
+    else if (part < 2 * KS)
+        tile_body<DVP, DKP, DVP, false, false, true>(t, &tm_v, &tm_o, &tm_q, t.R, p.dST, p.dk_, p.dk, p.k, slot, h, part - KS, part, 2 * KS);
+    else
+        tile_body<DKP, DKP, DVP, true, false, false>(t, &tm_k, &tm_q, &tm_o, t.R, p.dST, p.dv_, p.dv, nullptr, slot, h, part - 2 * KS, 0, 1);
+}
+
+// dg of a (chunk, head) by one warp, from the row sums q.dQ1, q.dQ2, k.dK1, k.dK2 (1: pairs within the chunk, 2:
+// through the states): the pairs within across t are the later rows' sums minus the later columns' (what both
+// count cancels, the diagonal included), the reads of the state from t on, the writes before t, and what passes.
+__global__ void __launch_bounds__(128) hla_dg_tc_kernel(const TileArgs t, int KS, long long units) {
+    const HlaArgs &p = t.a;
+    const long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (u >= units) return;
+    const long long slot = u / p.H;
+    const int h = (int)(u % p.H), lane = threadIdx.x & 31;
+    int n, c;
+    HlaSpan sp;
+    if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
+    const int Lc = min(C, sp.len - c * C);
+    const float *d = t.dots + (size_t)u * (2 * KS) * (2 * C);
+    double a[4], b[4];  // (sums in which larger terms cancel: fp64 costs nothing here)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = 4 * lane + e;
+        a[e] = b[e] = 0.0;
+        if (i < Lc)
+            for (int z = 0; z < KS; ++z) {
+                a[e] += ((double)d[(size_t)z * 2 * C + i] + (double)d[(size_t)z * 2 * C + C + i]) - (double)d[(size_t)(KS + z) * 2 * C + i];
+                b[e] += (double)d[(size_t)(KS + z) * 2 * C + C + i];
+            }
+    }
+    double sa = a[0] + a[1] + a[2] + a[3], sb = b[0] + b[1] + b[2] + b[3], after = sa, before = sb;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double x = __shfl_down_sync(0xffffffffu, after, off), y = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane + off < 32) after += x;
+        if (lane >= off) before += y;
+    }
+    double through = 0.0;
+    for (int z = 0; z < KS; ++z) through += (double)t.through[(size_t)u * KS + z];
+    double fa = after - sa, fb = before - sb;  // of the tokens of later lanes, and of earlier ones
+    fa += sa;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = 4 * lane + e;
+        if (i < Lc)
+            st_elem(static_cast<__nv_bfloat16 *>(p.dg), (size_t)(sp.t0 + (long long)c * C + i) * p.H + h, (float)(fa + fb + through));
+        fa -= a[e];
+        fb += b[e];
+    }
+}
+
+// ================================================================== host
+// 3-D map over a token-major [tokens, H, d] bf16 tensor; box of 64 channels (zeros past d) and 128 tokens.
+bool make_tile_map(CUtensorMap *m, const void *base, size_t tokens, int H, int d) {
+    auto enc = tc::get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)C};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Chunks per segment (0: whole sequences). The chains run one after another; where there are too few of them to
+// fill the GPU (three CTAs per SM), sequences are cut into segments that run side by side, at the price of a first
+// pass for their end states.
+int segment_chunks(const HlaArgs &a, int dirs) {
+    const long long chains = (long long)a.N * a.H * (padded(a.dk) / 64) * dirs, want = 3LL * device_sm_count();
+    const long long chunks = a.cu_seqlens ? (long long)a.T / C + 1 : ((long long)a.T + C - 1) / C;  // of the longest sequence, at most
+    if (chains * 2 > want || chunks < 16) return 0;
+    const long long total = chunks * (a.cu_seqlens ? 1 : a.N) * (chains / a.N);
+    const long long sc = (total + want - 1) / want;
+    return (int)(sc < 4 ? 4 : sc);
+}
+
+struct Layout {
+    int sc;
+    long long slots, seg_slots;
+    size_t blob[2], seg[2], keep[2], dots, through, bytes;
+};
+Layout layout(const HlaArgs &a, bool back) {
+    Layout l{};
+    const int dirs = back ? 2 : 1, dkp = padded(a.dk), dvp = padded(a.dv);
+    const bool packed = a.cu_seqlens != nullptr;
+    l.sc = segment_chunks(a, dirs);
+    l.slots = hla_slots(packed, a.N, a.T, C);
+    l.seg_slots = l.sc ? hla_slots(packed, a.N, a.T, l.sc * C) : 0;
+    size_t at = 0;
+    const auto take = [&](size_t bytes) { const size_t x = at; at += align256(bytes); return x; };
+    for (int d = 0; d < dirs; ++d) {
+        l.blob[d] = take((size_t)l.slots * a.H * blob_bytes(dkp, dvp));
+        l.seg[d] = take((size_t)l.seg_slots * a.H * a.dk * a.dv * 4);
+        l.keep[d] = take((size_t)l.seg_slots * a.H * 4);
+    }
+    if (back) {
+        l.dots = take((size_t)l.slots * a.H * (2 * dkp / 64) * 2 * C * 4);
+        l.through = take((size_t)l.slots * a.H * (dkp / 64) * 4);
+    }
+    l.bytes = at;
+    return l;
+}
+
+template <typename F>
+cudaError_t with_smem(F kern, size_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+struct Maps {
+    CUtensorMap q, k, v, o;
+};
+
+template <int DKP, int DVP>
+cudaError_t states(const StateArgs &s0, const Maps &m, const Layout &l, int dirs) {
+    const HlaArgs &a = s0.a;
+    const auto kern = hla_state_tc_kernel<DKP, DVP>;
+    constexpr size_t bytes = StateSmem<DVP>::bytes;
+    cudaError_t e = with_smem(kern, bytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), DKP / 64, dirs);
+    StateArgs s = s0;
+    if (l.sc) {
+        s.ends = true;
+        kern<<<grid, 128, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s, 0);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        hla_segment_scan_kernel<<<dim3((unsigned)(a.N * a.H), (a.dk * a.dv + 1023) / 1024, dirs), 256, 0, a.stream>>>(s, 0);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        s.ends = false;
+    }
+    kern<<<grid, 128, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s, 0);
+    return cudaGetLastError();
+}
+
+template <int DKP, int DVP>
+cudaError_t pass_t(const HlaArgs &a, bool back) {
+    const size_t tokens = (size_t)a.B * a.T;
+    Maps m;
+    if (!make_tile_map(&m.q, a.q, tokens, a.H, a.dk) || !make_tile_map(&m.k, a.k, tokens, a.H, a.dk) ||
+        !make_tile_map(&m.v, a.v, tokens, a.H, a.dv) || !make_tile_map(&m.o, back ? a.dO : a.v, tokens, a.H, a.dv))
+        return cudaErrorInvalidValue;
+    const Layout l = layout(a, back);
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    StateArgs s{};
+    s.a = a;
+    if (back) s.a.ST = nullptr;
+    s.sc = l.sc;
+    for (int d = 0; d < (back ? 2 : 1); ++d) {
+        s.blob[d] = ws + l.blob[d];
+        s.seg[d] = reinterpret_cast<float *>(ws + l.seg[d]);
+        s.seg_keep[d] = reinterpret_cast<float *>(ws + l.keep[d]);
+    }
+    cudaError_t e = states<DKP, DVP>(s, m, l, back ? 2 : 1);
+    if (e != cudaSuccess) return e;
+    TileArgs t{};
+    t.a = a;
+    t.S = s.blob[0];
+    t.R = s.blob[1];
+    const unsigned units = (unsigned)(l.slots * a.H);
+    if (!back) {
+        const auto kern = hla_out_tc_kernel<DKP, DVP>;
+        constexpr size_t bytes = TileSmem<DKP>::bytes;
+        if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
+        kern<<<units * (DVP / 64), 256, bytes, a.stream>>>(m.q, m.k, m.v, t);
+        return cudaGetLastError();
+    }
+    if (a.dg) {
+        t.dots = reinterpret_cast<float *>(ws + l.dots);
+        t.through = reinterpret_cast<float *>(ws + l.through);
+    }
+    const auto kern = hla_grad_tc_kernel<DKP, DVP>;
+    constexpr size_t b0 = TileSmem<DKP>::bytes, b1 = TileSmem<DVP>::bytes, bytes = b0 > b1 ? b0 : b1;
+    if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
+    kern<<<units * (2 * (DKP / 64) + DVP / 64), 256, bytes, a.stream>>>(m.q, m.k, m.v, m.o, t);
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.dg) return e;
+    hla_dg_tc_kernel<<<(units + 3) / 4, 128, 0, a.stream>>>(t, DKP / 64, units);
+    return cudaGetLastError();
+}
+
+cudaError_t pass(const HlaArgs &a, bool back) {
+    const int k = padded(a.dk), v = padded(a.dv);
+    if (k == 128) return v == 128 ? pass_t<128, 128>(a, back) : pass_t<128, 64>(a, back);
+    return v == 128 ? pass_t<64, 128>(a, back) : pass_t<64, 64>(a, back);
+}
+
+}  // namespace
+
+bool hla_tc_supported(const HlaArgs &a) {
+    // one tile per (chunk slot, head, slice of a result), in a 31-bit grid
+    return a.dtype == KDA_DTYPE_BF16 && hla_slots(a.cu_seqlens != nullptr, a.N, a.T, C) <= 0x7fffffffLL / 6 / a.H;
+}
+size_t hla_tc_workspace(const HlaArgs &a, bool back) { return layout(a, back).bytes; }
+cudaError_t launch_hla_forward_tc(const HlaArgs &a) { return pass(a, false); }
+cudaError_t launch_hla_backward_tc(const HlaArgs &a) { return pass(a, true); }
+
+}  // namespace kda
