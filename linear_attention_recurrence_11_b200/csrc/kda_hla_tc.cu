@@ -4,11 +4,7 @@
 //
 // Two steps. The state kernel carries the state (and, for the backward pass, its gradient from the
 // last chunk to the first) over the chunks and leaves each chunk's incoming one in the workspace as a
-// bf16 operand tile. The tile kernels then take every (chunk, head) on its own: with X, Y, Z tiles of
-// the chunk and W a state,
-//     out = c1 (X Y^T . D) Z + c2 X W,       c2 per row,
-// which is the output (X, Y, Z, W = Q, K, V, S) and each of the gradients dQ (dO, V, K, S),
-// dK (V, dO, Q, R) and dV (K, Q, dO, R), the last two with D transposed.
+// bf16 operand tile. The tile kernels then take every (chunk, head) on its own.
 //
 // Roundings to bf16: the masked scores (as the operand of the second product), the states (as an
 // operand; they are carried in fp32), and the results. The state's own update multiplies k v^T by a
@@ -265,30 +261,29 @@ __global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s
 // ================================================================== tiles
 struct TileArgs {
     HlaArgs a;
-    const uint8_t *S, *R;   // the chunks' states and their gradients
-    float *dots;            // [slot][H][parts][2][128]: partial row sums for dg (null: not wanted)
-    float *through;         // [slot][H][dk slices]
+    const uint8_t *S, *R;   // the chunks' incoming states, and the gradients of their outgoing ones
 };
 
-// Shared memory of a tile: X, Y (XD channels), Z (64 channels), W (64 columns of the result), the
-// scores (over Y where that has room), and G.
+// ------------------------------------------------------------------ outputs
+// O = scale [(Q K^T . D) V + e^{G_r} Q S]. One CTA per chunk, head and 64 columns of dv.
 template <int XD>
-struct TileSmem {
-    static constexpr uint32_t X = 0, Y = (XD / 64) * TILE, P = XD == 128 ? Y : Y + TILE;
+struct OutTile {
+    static constexpr uint32_t X = 0, Y = (XD / 64) * TILE, P = XD == 128 ? Y : Y + TILE;  // the scores go over K where it has room
     static constexpr uint32_t Z = P + 2 * TILE, W = Z + TILE, MISC = W + (XD / 64) * 8 * KB;
-    static constexpr uint32_t G = MISC + 64, RED = G + C * 8;   // RED: 2 x 128 float2, and 8 floats
-    static constexpr uint32_t bytes = RED + 2 * C * 8 + 64 + 1024;
+    static constexpr uint32_t G = MISC + 64;
+    static constexpr uint32_t bytes = G + C * 8 + 1024;
 };
 
-// kKMajor: the state's rows (dv) are the result's columns (outputs, dV); else its dk are (dQ, dK).
-// kLower: D_rs for s <= r, and c2 = scale e^{G_r}; else D_sr for s >= r, and c2 = e^{G_C - G_r}.
-// z: 64-column slice of the result.
-template <int XD, int DKP, int DVP, bool kKMajor, bool kLower, bool kDots>
-__device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUtensorMap *tmY, const CUtensorMap *tmZ, const uint8_t *blobs,
-                          const float *border, void *out, int out_d, const void *dot_src, long long slot, int h, int z, int part,
-                          int parts) {
-    using L = TileSmem<XD>;
+template <int DKP, int DVP>
+__global__ void __launch_bounds__(256, 2) hla_out_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                                                            const __grid_constant__ CUtensorMap tm_v, const TileArgs t) {
+    using L = OutTile<DKP>;
     const HlaArgs &p = t.a;
+    constexpr int parts = DVP / 64;
+    const int z = blockIdx.x % parts;
+    const unsigned u = blockIdx.x / parts;
+    const long long slot = u / p.H;
+    const int h = u % p.H;
     int n, c;
     HlaSpan sp;
     if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
@@ -302,8 +297,7 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, half = warp >> 2;
     const long long row0 = sp.t0 + (long long)c * C;
     const int Lc = min(C, sp.len - c * C);
-    const bool has = border != nullptr || (kLower ? c > 0 : c + 1 < sp.nch);  // a state that is not all zeros
-    constexpr uint32_t WB = (XD / 64) * 8 * KB;  // the state's slice: 64 rows of XD, or XD rows of 64
+    const bool has = p.S0 != nullptr || c > 0;  // a state that is not all zeros
 
     if (tid == 0) {
         mbar_init(bar_xy, 1);
@@ -312,23 +306,18 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
         mbar_init(bar_o, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(bar_xy, 2 * (XD / 64) * TILE);
+        mbar_arrive_expect_tx(bar_xy, 2 * (DKP / 64) * TILE);
 #pragma unroll
-        for (int b = 0; b < XD / 64; ++b) {
-            tma_load_3d(sm + L::X + b * TILE, tmX, bar_xy, 64 * b, h, (int)row0);
-            tma_load_3d(sm + L::Y + b * TILE, tmY, bar_xy, 64 * b, h, (int)row0);
+        for (int b = 0; b < DKP / 64; ++b) {
+            tma_load_3d(sm + L::X + b * TILE, &tm_q, bar_xy, 64 * b, h, (int)row0);
+            tma_load_3d(sm + L::Y + b * TILE, &tm_k, bar_xy, 64 * b, h, (int)row0);
         }
-        mbar_arrive_expect_tx(bar_zw, TILE + (has ? WB : 0u));
-        tma_load_3d(sm + L::Z, tmZ, bar_zw, 64 * z, h, (int)row0);
-        if (has) {
-            const uint8_t *src = blobs + ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP);
-            if (kKMajor) {  // rows 64 z .. + 63 of every block of 64 dk
+        mbar_arrive_expect_tx(bar_zw, TILE + (has ? (DKP / 64) * 8 * KB : 0u));
+        tma_load_3d(sm + L::Z, &tm_v, bar_zw, 64 * z, h, (int)row0);
+        if (has) {  // rows 64 z .. + 63 of every block of 64 dk
+            const uint8_t *src = t.S + ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP) + (size_t)z * 8 * KB;
 #pragma unroll
-                for (int b = 0; b < XD / 64; ++b)
-                    bulk_load(sm + L::W + b * 8 * KB, src + (size_t)b * DVP * 128 + (size_t)z * 8 * KB, 8 * KB, bar_zw);
-            } else {        // block z of dk: all dv rows
-                bulk_load(sm + L::W, src + (size_t)z * DVP * 128, WB, bar_zw);
-            }
+            for (int b = 0; b < DKP / 64; ++b) bulk_load(sm + L::W + b * 8 * KB, src + (size_t)b * DVP * 128, 8 * KB, bar_zw);
         }
     }
     if (warp == 0) {
@@ -341,38 +330,25 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem, tlane = (uint32_t)(32 * quarter) << 16;
-    constexpr uint32_t TS = 0, T1 = 128, T2 = 192;  // scores, (scores) Z, X W
+    constexpr uint32_t TS = 0, T1 = 128, T2 = 192;  // scores, (scores) V, Q S
 
     bool ok = true;
     if (tid == 0) {
         ok = mbar_wait_bounded(bar_xy, 0, kWaitCycles);
         if (ok) {
-            mma_chain<XD / 16>(tmem + TS, Opnd{sbase + L::X, false, TILE, 0}, Opnd{sbase + L::Y, false, TILE, 0},
-                               idesc_bf16_f32(128, 128, 0, 0), false);
+            mma_chain<DKP / 16>(tmem + TS, Opnd{sbase + L::X, false, TILE, 0}, Opnd{sbase + L::Y, false, TILE, 0},
+                                idesc_bf16_f32(128, 128, 0, 0), false);
             mma_commit(bar_s);
         }
     }
     __syncwarp();
     const bool ok_zw = mbar_wait_bounded(bar_zw, 0, kWaitCycles);
     if (tid == 0 && ok && ok_zw && has)
-        mma_chain<XD / 16>(tmem + T2, Opnd{sbase + L::X, false, TILE, 0},
-                           Opnd{sbase + L::W, !kKMajor, 8 * KB, 0}, idesc_bf16_f32(128, 64, 0, kKMajor ? 0 : 1), false);
-    if (Lc < C && ok_zw) {  // rows of Z behind the sequence's end: zero, whatever stands there
+        mma_chain<DKP / 16>(tmem + T2, Opnd{sbase + L::X, false, TILE, 0}, Opnd{sbase + L::W, false, 8 * KB, 0},
+                            idesc_bf16_f32(128, 64, 0, 0), false);
+    if (Lc < C && ok_zw) {  // rows of V behind the sequence's end: zero, whatever stands there
         for (int i = tid; i < (C - Lc) * 8; i += 256)
             *reinterpret_cast<uint4 *>(sm + L::Z + sw128_offset(Lc + (i >> 3), 8 * (i & 7))) = make_uint4(0, 0, 0, 0);
-    }
-    float thr = 0.f;
-    if (kDots && !kLower && t.dots && ok_zw && has && (c > 0 || p.S0)) {  // <S, R> over this slice
-        const uint8_t *S = t.S + ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP) + (size_t)z * DVP * 128;
-#pragma unroll
-        for (int i = 0; i < (int)(WB / 16 / 256); ++i) {
-            const uint32_t off = 16u * (tid + 256 * i);
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(S + off)), b = *reinterpret_cast<const uint4 *>(sm + L::W + off);
-            thr = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), thr));
-            thr = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), thr));
-            thr = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), thr));
-            thr = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), thr));
-        }
     }
     __syncwarp();
     const bool ok_s = mbar_wait_bounded(bar_s, 0, kWaitCycles);
@@ -386,9 +362,7 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
         for (int q = 0; q < 4; ++q) {
             const int s0 = 64 * half + 16 * q;
             uint32_t w[8];
-            // a block of 32 rows and 16 columns that the mask leaves nothing of is not computed
-            const bool none = kLower ? s0 > 32 * quarter + 31 : s0 + 15 < 32 * quarter;
-            if (none) {
+            if (s0 > 32 * quarter + 31) {  // 32 rows and 16 columns that the mask leaves nothing of
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = 0u;
             } else {
@@ -396,12 +370,7 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
                 tmem_ld16(tmem + tlane + TS + s0, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int s = s0 + e;
-                    const float2 gs = G[s];
-                    const float d = kLower ? hla_decay(gr, gs) : hla_decay(gs, gr);
-                    v[e] = (kLower ? s <= r : s >= r && s < Lc) ? v[e] * d : 0.f;
-                }
+                for (int e = 0; e < 16; ++e) v[e] = s0 + e <= r ? v[e] * hla_decay(gr, G[s0 + e]) : 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = pack_bf2(v[2 * e], v[2 * e + 1]);
             }
@@ -426,12 +395,9 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
         tc_fence_after();
     }
     if (ok_o) {
-        const float2 g0 = make_float2(0.f, 0.f);
-        const float c2 = kLower ? p.scale * hla_decay(gr, g0) : hla_decay(G[C - 1], gr);
+        const float c2 = p.scale * hla_decay(gr, make_float2(0.f, 0.f));
         const int col = 64 * z + 32 * half;
-        const bool live = r < Lc && col < out_d;
-        const size_t at = ((size_t)(row0 + r) * p.H + h) * out_d + col;
-        float d1 = 0.f, d2 = 0.f;
+        const size_t at = ((size_t)(row0 + r) * p.H + h) * p.dv + col;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float v1[16], v2[16];
@@ -439,55 +405,16 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
             if (has) tmem_ld16(tmem + tlane + T2 + 32u * half + 16u * q, v2);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                v1[e] *= p.scale;
-                v2[e] = has ? v2[e] * c2 : 0.f;
-            }
-            if (live) {
-                if (kDots && t.dots) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(dot_src) + at + 16 * q);
-                    const uint4 a = __ldg(src), b = __ldg(src + 1);
-                    const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        d1 = fmaf(v1[2 * e], bf_lo(in[e]), fmaf(v1[2 * e + 1], bf_hi(in[e]), d1));
-                        d2 = fmaf(v2[2 * e], bf_lo(in[e]), fmaf(v2[2 * e + 1], bf_hi(in[e]), d2));
-                    }
-                }
-                uint32_t w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = pack_bf2(v1[2 * e] + v2[2 * e], v1[2 * e + 1] + v2[2 * e + 1]);
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at + 16 * q);
-                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-        }
-        if (kDots && t.dots) {
-            float2 *red = reinterpret_cast<float2 *>(sm + L::RED);
-            red[half * C + r] = make_float2(d1, d2);
-            if (!kLower) {
-#pragma unroll
-                for (int off = 16; off; off >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, off);
-                if (lane == 0) reinterpret_cast<float *>(red + 2 * C)[warp] = thr;
+            for (int e = 0; e < 16; ++e) v1[e] = has ? fmaf(p.scale, v1[e], c2 * v2[e]) : p.scale * v1[e];
+            if (r < Lc && col < p.dv) {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at + 16 * q);
+                dst[0] = make_uint4(pack_bf2(v1[0], v1[1]), pack_bf2(v1[2], v1[3]), pack_bf2(v1[4], v1[5]), pack_bf2(v1[6], v1[7]));
+                dst[1] = make_uint4(pack_bf2(v1[8], v1[9]), pack_bf2(v1[10], v1[11]), pack_bf2(v1[12], v1[13]), pack_bf2(v1[14], v1[15]));
             }
         }
     }
     tc_fence_before();
     const bool failed = __syncthreads_or(!ok_o);
-    if (kDots && t.dots && !failed) {
-        const float2 *red = reinterpret_cast<const float2 *>(sm + L::RED);
-        float *dst = t.dots + (((size_t)slot * p.H + h) * parts + part) * (2 * C);
-        if (tid < C) {
-            dst[tid] = red[tid].x + red[C + tid].x;
-            dst[C + tid] = red[tid].y + red[C + tid].y;
-        }
-        if (!kLower && tid == 0) {
-            float u = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u += reinterpret_cast<const float *>(red + 2 * C)[i];
-            t.through[((size_t)slot * p.H + h) * (DKP / 64) + z] = hla_decay(G[C - 1], make_float2(0.f, 0.f)) * u;
-        }
-    }
     if (failed && tid == 0) {  // leave nothing in flight behind
         if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
         mbar_wait_bounded(bar_xy, 0, kWaitCycles);
@@ -502,77 +429,359 @@ __device__ void tile_body(const TileArgs &t, const CUtensorMap *tmX, const CUten
     }
 }
 
+// ---------------------------------------------------------------- gradients
+// All gradients of a (chunk, head), by one CTA of 512 threads. With P = Q K^T and dP = dO V^T (both [row r, column
+// s], so that one decay D_rs serves both), A = scale P . D and dA = scale dP . D in bf16:
+//   dQ = dA K   + scale e^{G_r} dO S      accumulators T2
+//   dK = dA^T Q + e^{G_C - G_r} V R       T3
+//   dV = A^T dO + e^{G_C - G_r} K R^T     T1 (dP's, once that is read)
+// The product with the state comes first; the threads scale its rows in TMEM, and the other product accumulates on
+// top. A and dA go over S and V, which are free by then. dg comes from row sums in fp32 (below).
 template <int DKP, int DVP>
-__global__ void __launch_bounds__(256, 2) hla_out_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                                                            const __grid_constant__ CUtensorMap tm_v, const TileArgs t) {
-    constexpr int parts = DVP / 64;
-    const int z = blockIdx.x % parts;
-    const unsigned u = blockIdx.x / parts;
-    tile_body<DKP, DKP, DVP, true, true, false>(t, &tm_q, &tm_k, &tm_v, t.S, t.a.S0, t.a.o, t.a.dv, nullptr, u / t.a.H, u % t.a.H, z, 0, 1);
-}
+struct GradTile {
+    static constexpr uint32_t QB = (DKP / 64) * TILE, VB = (DVP / 64) * TILE, SB = DKP * DVP * 2;
+    static constexpr bool over = DKP == 128 && DVP == 128;
+    static constexpr uint32_t Q = 0, K = QB, V = 2 * QB, O = V + VB, S = O + VB, R = S + SB;
+    static constexpr uint32_t A = over ? S : R + SB, dA = over ? V : A + 2 * TILE, END = over ? R + SB : dA + 2 * TILE;
+    static constexpr uint32_t G = END + 128, RED = G + C * 8;          // RED: 3 x 4 x 128 floats, and 16
+    static constexpr uint32_t bytes = RED + 12 * C * 4 + 64 + 1024;
+    static_assert(bytes <= 232448, "shared memory budget");
+};
 
-// The slices of dQ, dK and dV of a (chunk, head) are neighbours in the grid: they read the same tiles, from L2.
 template <int DKP, int DVP>
-__global__ void __launch_bounds__(256, 2) hla_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+__global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                                                              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                                                             const TileArgs t) {
-    constexpr int KS = DKP / 64, VS = DVP / 64, parts = 2 * KS + VS;
+                                                             const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
+                                                             const __grid_constant__ CUtensorMap tm_dv, const TileArgs t) {
+    using L = GradTile<DKP, DVP>;
     const HlaArgs &p = t.a;
-    const int part = blockIdx.x % parts;
-    const unsigned u = blockIdx.x / parts;
-    const long long slot = u / p.H;
-    const int h = u % p.H;
-    if (part < KS)
-        tile_body<DVP, DKP, DVP, false, true, true>(t, &tm_o, &tm_v, &tm_k, t.S, p.S0, p.dq, p.dk, p.q, slot, h, part, part, 2 * KS);
-    else if (part < 2 * KS)
-        tile_body<DVP, DKP, DVP, false, false, true>(t, &tm_v, &tm_o, &tm_q, t.R, p.dST, p.dk_, p.dk, p.k, slot, h, part - KS, part, 2 * KS);
-    else
-        tile_body<DKP, DKP, DVP, true, false, false>(t, &tm_k, &tm_q, &tm_o, t.R, p.dST, p.dv_, p.dv, nullptr, slot, h, part - 2 * KS, 0, 1);
-}
-
-// dg of a (chunk, head) by one warp, from the row sums q.dQ1, q.dQ2, k.dK1, k.dK2 (1: pairs within the chunk, 2:
-// through the states): the pairs within across t are the later rows' sums minus the later columns' (what both
-// count cancels, the diagonal included), the reads of the state from t on, the writes before t, and what passes.
-__global__ void __launch_bounds__(128) hla_dg_tc_kernel(const TileArgs t, int KS, long long units) {
-    const HlaArgs &p = t.a;
-    const long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (u >= units) return;
-    const long long slot = u / p.H;
-    const int h = (int)(u % p.H), lane = threadIdx.x & 31;
+    const long long slot = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H;
     int n, c;
     HlaSpan sp;
     if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(sm);
+    // loads: q k, v dO, S R; products: P, dP, dO S and V R, K R^T, dA K and dA^T Q, A^T dO
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::END);
+    enum { L_QK, L_VO, L_SR, B_P, B_DP, B_SR, B_KR, B_QK, B_V, NBAR };
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + NBAR);
+    float2 *G = reinterpret_cast<float2 *>(sm + L::G);
+    float *red = reinterpret_cast<float *>(sm + L::RED);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, grp = warp >> 2;
+    const long long row0 = sp.t0 + (long long)c * C;
     const int Lc = min(C, sp.len - c * C);
-    const float *d = t.dots + (size_t)u * (2 * KS) * (2 * C);
-    double a[4], b[4];  // (sums in which larger terms cancel: fp64 costs nothing here)
+    const bool hasS = p.S0 != nullptr || c > 0, hasR = p.dST != nullptr || c + 1 < sp.nch;
+
+    if (tid == 0) {
+        for (int i = 0; i < NBAR; ++i) mbar_init(bars + i, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(bars + L_QK, 2 * L::QB);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int i = 4 * lane + e;
-        a[e] = b[e] = 0.0;
-        if (i < Lc)
-            for (int z = 0; z < KS; ++z) {
-                a[e] += ((double)d[(size_t)z * 2 * C + i] + (double)d[(size_t)z * 2 * C + C + i]) - (double)d[(size_t)(KS + z) * 2 * C + i];
-                b[e] += (double)d[(size_t)(KS + z) * 2 * C + C + i];
+        for (int b = 0; b < DKP / 64; ++b) {
+            tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + L_QK, 64 * b, h, (int)row0);
+            tma_load_3d(sm + L::K + b * TILE, &tm_k, bars + L_QK, 64 * b, h, (int)row0);
+        }
+        mbar_arrive_expect_tx(bars + L_VO, 2 * L::VB);
+#pragma unroll
+        for (int b = 0; b < DVP / 64; ++b) {
+            tma_load_3d(sm + L::V + b * TILE, &tm_v, bars + L_VO, 64 * b, h, (int)row0);
+            tma_load_3d(sm + L::O + b * TILE, &tm_o, bars + L_VO, 64 * b, h, (int)row0);
+        }
+        mbar_arrive_expect_tx(bars + L_SR, (hasS ? L::SB : 0u) + (hasR ? L::SB : 0u));
+        const size_t at = ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP);
+        if (hasS) bulk_load(sm + L::S, t.S + at, L::SB, bars + L_SR);
+        if (hasR) bulk_load(sm + L::R, t.R + at, L::SB, bars + L_SR);
+    }
+    if (warp == 0) {
+        __syncwarp();
+        tmem_alloc(s_tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 1) hla_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem, tlane = (uint32_t)(32 * quarter) << 16;
+    constexpr uint32_t T0 = 0, T1 = 128, T2 = 256, T3 = 384;
+    const int r = 32 * quarter + lane, col = 32 * grp;   // this thread's row, and its 32 columns
+    const float2 g0 = make_float2(0.f, 0.f), gr = G[r];
+    const auto zero16 = [&](uint32_t off) { *reinterpret_cast<uint4 *>(sm + off) = make_uint4(0, 0, 0, 0); };
+
+    bool ok = true;
+    const auto wait = [&](int b) { ok = mbar_wait_bounded(bars + b, 0, kWaitCycles) && ok; };
+    if (Lc < C) {  // rows behind the sequence's end: zero in every operand, whatever stands there
+        wait(L_QK);
+        wait(L_VO);
+        for (int i = tid; i < (C - Lc) * 8; i += 512) {
+            const uint32_t off = sw128_offset(Lc + (i >> 3), 8 * (i & 7));
+#pragma unroll
+            for (int b = 0; b < DKP / 64; ++b) {
+                zero16(L::Q + b * TILE + off);
+                zero16(L::K + b * TILE + off);
             }
-    }
-    double sa = a[0] + a[1] + a[2] + a[3], sb = b[0] + b[1] + b[2] + b[3], after = sa, before = sb;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const double x = __shfl_down_sync(0xffffffffu, after, off), y = __shfl_up_sync(0xffffffffu, before, off);
-        if (lane + off < 32) after += x;
-        if (lane >= off) before += y;
+            for (int b = 0; b < DVP / 64; ++b) {
+                zero16(L::V + b * TILE + off);
+                zero16(L::O + b * TILE + off);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
     }
-    double through = 0.0;
-    for (int z = 0; z < KS; ++z) through += (double)t.through[(size_t)u * KS + z];
-    double fa = after - sa, fb = before - sb;  // of the tokens of later lanes, and of earlier ones
-    fa += sa;
+    const Opnd oQ{sbase + L::Q, false, TILE, 0}, oK{sbase + L::K, false, TILE, 0}, oV{sbase + L::V, false, TILE, 0}, oO{sbase + L::O, false, TILE, 0};
+    if (tid == 0) {
+        wait(L_QK);
+        if (ok) {
+            mma_chain<DKP / 16>(tmem + T0, oQ, oK, idesc_bf16_f32(128, 128, 0, 0), false);
+            mma_commit(bars + B_P);
+        }
+        wait(L_VO);
+        if (ok) {
+            mma_chain<DVP / 16>(tmem + T1, oO, oV, idesc_bf16_f32(128, 128, 0, 0), false);
+            mma_commit(bars + B_DP);
+        }
+        wait(L_SR);
+        if (ok) {  // S, R as [dv rows][dk]: dk is the result's column
+            if (hasS) mma_chain<DVP / 16>(tmem + T2, oO, Opnd{sbase + L::S, true, 0, DVP * 128}, idesc_bf16_f32(128, DKP, 0, 1), false);
+            if (hasR) mma_chain<DVP / 16>(tmem + T3, oV, Opnd{sbase + L::R, true, 0, DVP * 128}, idesc_bf16_f32(128, DKP, 0, 1), false);
+            mma_commit(bars + B_SR);
+        }
+    }
+    __syncwarp();
+    float thr = 0.f;
+    if (p.dg && hasS && hasR) {  // <S, R>
+        wait(L_SR);
+        if (ok) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int i = 4 * lane + e;
-        if (i < Lc)
-            st_elem(static_cast<__nv_bfloat16 *>(p.dg), (size_t)(sp.t0 + (long long)c * C + i) * p.H + h, (float)(fa + fb + through));
-        fa -= a[e];
-        fb += b[e];
+            for (int i = 0; i < (int)(L::SB / 16 / 512); ++i) {
+                const uint32_t off = 16u * (tid + 512 * i);
+                const uint4 a = *reinterpret_cast<const uint4 *>(sm + L::S + off), b = *reinterpret_cast<const uint4 *>(sm + L::R + off);
+                thr = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), thr));
+                thr = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), thr));
+                thr = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), thr));
+                thr = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), thr));
+            }
+        }
+    }
+    // A and dA of this thread's row and columns, in bf16 pairs
+    uint32_t wa[16], wd[16];
+    wait(B_P);
+    wait(B_DP);
+    tc_fence_after();
+    if (col > 32 * quarter + 31) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) wa[e] = wd[e] = 0u;
+    } else if (ok) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float a[16], d[16];
+            tmem_ld16(tmem + tlane + T0 + col + 16u * q, a);
+            tmem_ld16(tmem + tlane + T1 + col + 16u * q, d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int s = col + 16 * q + e;
+                const float x = p.scale * hla_decay(gr, G[s]);
+                const bool in = s <= r && r < Lc;
+                a[e] = in ? a[e] * x : 0.f;
+                d[e] = in ? d[e] * x : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                wa[8 * q + e] = pack_bf2(a[2 * e], a[2 * e + 1]);
+                wd[8 * q + e] = pack_bf2(d[2 * e], d[2 * e + 1]);
+            }
+        }
+    }
+    wait(B_SR);  // the products have read S and V ..
+    __syncthreads();  // .. and every thread its part of S
+    if (ok) {
+        uint8_t *da = sm + L::A + (col >> 6) * TILE, *dd = sm + L::dA + (col >> 6) * TILE;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t off = sw128_offset(r, (col & 63) + 8 * q);
+            *reinterpret_cast<uint4 *>(da + off) = make_uint4(wa[4 * q], wa[4 * q + 1], wa[4 * q + 2], wa[4 * q + 3]);
+            *reinterpret_cast<uint4 *>(dd + off) = make_uint4(wd[4 * q], wd[4 * q + 1], wd[4 * q + 2], wd[4 * q + 3]);
+        }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    // the state's products scaled per row in TMEM; sums of k . dK2 on the way
+    const float since = p.scale * hla_decay(gr, g0), until = hla_decay(G[C - 1], gr);
+    float cs2 = 0.f, cs = 0.f, rs = 0.f;
+    const auto dot16 = [&](uint32_t tile, int cl, const float (&v)[16]) {
+        float x = 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(sm + tile + (cl >> 6) * TILE + sw128_offset(r, (cl & 63) + 8 * q));
+            const uint32_t in[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x = fmaf(bf_lo(in[e]), v[8 * q + 2 * e], fmaf(bf_hi(in[e]), v[8 * q + 2 * e + 1], x));
+        }
+        return x;
+    };
+    const auto scale_rows = [&](uint32_t T, float f) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float v[16];
+            tmem_ld16(tmem + tlane + T + col + 16u * q, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= f;
+            tmem_st16(tmem + tlane + T + col + 16u * q, v);
+            if (T == T3 && p.dg) cs2 += dot16(L::K, col + 16 * q, v);
+        }
+        tmem_wait_st();
+    };
+    bool bad = __syncthreads_or(!ok);
+    if (!bad) {
+        if (tid == 0) {
+            tc_fence_after();
+            if (hasR) mma_chain<DKP / 16>(tmem + T1, oK, Opnd{sbase + L::R, false, DVP * 128, 0}, idesc_bf16_f32(128, DVP, 0, 0), false);
+            mma_commit(bars + B_KR);
+        }
+        __syncwarp();
+        tc_fence_after();
+        if (hasS && col < DKP) scale_rows(T2, since);
+        if (hasR && col < DKP) scale_rows(T3, until);
+        tc_fence_before();
+        __syncthreads();
+        const Opnd aT{sbase + L::A, true, 0, TILE}, dT{sbase + L::dA, true, 0, TILE}, dN{sbase + L::dA, false, TILE, 0};
+        if (tid == 0) {
+            tc_fence_after();
+            mma_chain<C / 16>(tmem + T2, dN, Opnd{sbase + L::K, true, 0, TILE}, idesc_bf16_f32(128, DKP, 0, 1), hasS);
+            mma_chain<C / 16>(tmem + T3, dT, Opnd{sbase + L::Q, true, 0, TILE}, idesc_bf16_f32(128, DKP, 1, 1), hasR);
+            mma_commit(bars + B_QK);
+        }
+        __syncwarp();
+        wait(B_KR);
+        tc_fence_after();
+        if (ok && hasR && col < DVP) scale_rows(T1, until);
+        tc_fence_before();
+        bad = __syncthreads_or(!ok);
+        if (!bad) {
+            if (tid == 0) {
+                tc_fence_after();
+                mma_chain<C / 16>(tmem + T1, aT, Opnd{sbase + L::O, true, 0, TILE}, idesc_bf16_f32(128, DVP, 1, 1), hasR);
+                mma_commit(bars + B_V);
+            }
+            __syncwarp();
+        }
+    }
+    // results: staged over q, k and (dA, or v), written by tensor stores; rows of a partial chunk directly
+    const auto result = [&](uint32_t T, uint32_t stage, void *out, int d, float *sum) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float v[16];
+            const int cl = col + 16 * q;
+            tmem_ld16(tmem + tlane + T + cl, v);
+            tmem_wait_ld();
+            if (sum && p.dg) *sum += dot16(stage, cl, v);
+            const uint4 w0 = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
+            const uint4 w1 = make_uint4(pack_bf2(v[8], v[9]), pack_bf2(v[10], v[11]), pack_bf2(v[12], v[13]), pack_bf2(v[14], v[15]));
+            if (Lc == C) {  // (each thread replaces the elements that it alone has read)
+                uint8_t *dst = sm + stage + (cl >> 6) * TILE;
+                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, cl & 63)) = w0;
+                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, (cl & 63) + 8)) = w1;
+            } else if (r < Lc && cl < d) {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + ((size_t)(row0 + r) * p.H + h) * d + cl);
+                dst[0] = w0;
+                dst[1] = w1;
+            }
+        }
+    };
+    if (!bad) {
+        wait(B_QK);
+        tc_fence_after();
+        if (ok && col < DKP) {
+            result(T2, L::Q, p.dq, p.dk, &rs);
+            result(T3, L::K, p.dk_, p.dk, &cs);
+        }
+        if (p.dg) {
+            red[grp * C + r] = rs;
+            red[(4 + grp) * C + r] = cs;
+            red[(8 + grp) * C + r] = cs2;
+#pragma unroll
+            for (int off = 16; off; off >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, off);
+            if (lane == 0) red[12 * C + warp] = thr;
+        }
+        fence_proxy_async_smem();
+        bad = __syncthreads_or(!ok);
+    }
+    if (!bad) {
+        if (Lc == C && tid == 0) {
+#pragma unroll
+            for (int b = 0; b < DKP / 64; ++b) {
+                tma_store_3d(&tm_dq, sm + L::Q + b * TILE, 64 * b, h, (int)row0);
+                tma_store_3d(&tm_dk, sm + L::K + b * TILE, 64 * b, h, (int)row0);
+            }
+            bulk_commit();
+        }
+        __syncwarp();
+        // dg by one warp: what a token from t on reads of one before t. Within the chunk: the later rows' sums
+        // q . dQ less the later columns' sums k . dK1 (pairs that both count, the diagonal among them, cancel; the
+        // rows' sums hold the reads of S too); the earlier columns' k . dK2; and e^{G_C} <S, R>.
+        if (p.dg && warp == 2) {
+            double a[4], b[4];  // (larger terms cancel: fp64, of a few hundred numbers)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * lane + e;
+                double x[3];
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    x[k] = ((double)red[(4 * k) * C + i] + (double)red[(4 * k + 1) * C + i]) + ((double)red[(4 * k + 2) * C + i] + (double)red[(4 * k + 3) * C + i]);
+                a[e] = x[0] - (x[1] - x[2]);
+                b[e] = x[2];
+            }
+            double after = (a[0] + a[1]) + (a[2] + a[3]), before = (b[0] + b[1]) + (b[2] + b[3]), fb = before, through = 0.0;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const double x = __shfl_down_sync(0xffffffffu, after, off), y = __shfl_up_sync(0xffffffffu, before, off);
+                if (lane + off < 32) after += x;
+                if (lane >= off) before += y;
+            }
+            fb = before - fb;
+            for (int w = 0; w < 16; ++w) through += (double)red[12 * C + w];
+            through *= (double)hla_decay(G[C - 1], g0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * lane + e;
+                if (i < Lc) st_elem(static_cast<__nv_bfloat16 *>(p.dg), (size_t)(row0 + i) * p.H + h, (float)(after + fb + through));
+                after -= a[e];
+                fb += b[e];
+            }
+        }
+        wait(B_V);
+        tc_fence_after();
+        const uint32_t stage = L::over ? L::dA : L::V;
+        if (ok && col < DVP) result(T1, stage, p.dv_, p.dv, nullptr);
+        fence_proxy_async_smem();
+        bad = __syncthreads_or(!ok);
+        if (!bad && Lc == C && tid == 0) {
+#pragma unroll
+            for (int b = 0; b < DVP / 64; ++b) tma_store_3d(&tm_dv, sm + stage + b * TILE, 64 * b, h, (int)row0);
+            bulk_commit();
+        }
+    }
+    if (tid == 0) bulk_wait_all();
+    tc_fence_before();
+    if (bad && tid == 0) {  // leave nothing in flight behind: the copies, and whatever products were issued
+        if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
+        mbar_wait_bounded(bars + L_QK, 0, kWaitCycles);
+        mbar_wait_bounded(bars + L_VO, 0, kWaitCycles);
+        mbar_wait_bounded(bars + L_SR, 0, kWaitCycles);
+        uint64_t *spare = bars + L_QK;  // its copies are done: a second phase, completed by the last product
+        mma_commit(spare);
+        mbar_wait_bounded(spare, 1, kWaitCycles);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -606,7 +815,7 @@ int segment_chunks(const HlaArgs &a, int dirs) {
 struct Layout {
     int sc;
     long long slots, seg_slots;
-    size_t blob[2], seg[2], keep[2], dots, through, bytes;
+    size_t blob[2], seg[2], keep[2], bytes;
 };
 Layout layout(const HlaArgs &a, bool back) {
     Layout l{};
@@ -622,10 +831,6 @@ Layout layout(const HlaArgs &a, bool back) {
         l.seg[d] = take((size_t)l.seg_slots * a.H * a.dk * a.dv * 4);
         l.keep[d] = take((size_t)l.seg_slots * a.H * 4);
     }
-    if (back) {
-        l.dots = take((size_t)l.slots * a.H * (2 * dkp / 64) * 2 * C * 4);
-        l.through = take((size_t)l.slots * a.H * (dkp / 64) * 4);
-    }
     l.bytes = at;
     return l;
 }
@@ -636,7 +841,7 @@ cudaError_t with_smem(F kern, size_t bytes) {
 }
 
 struct Maps {
-    CUtensorMap q, k, v, o;
+    CUtensorMap q, k, v, o, dq, dk, dv;
 };
 
 template <int DKP, int DVP>
@@ -667,6 +872,9 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     if (!make_tile_map(&m.q, a.q, tokens, a.H, a.dk) || !make_tile_map(&m.k, a.k, tokens, a.H, a.dk) ||
         !make_tile_map(&m.v, a.v, tokens, a.H, a.dv) || !make_tile_map(&m.o, back ? a.dO : a.v, tokens, a.H, a.dv))
         return cudaErrorInvalidValue;
+    if (back && (!make_tile_map(&m.dq, a.dq, tokens, a.H, a.dk) || !make_tile_map(&m.dk, a.dk_, tokens, a.H, a.dk) ||
+                 !make_tile_map(&m.dv, a.dv_, tokens, a.H, a.dv)))
+        return cudaErrorInvalidValue;
     const Layout l = layout(a, back);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     StateArgs s{};
@@ -687,21 +895,15 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     const unsigned units = (unsigned)(l.slots * a.H);
     if (!back) {
         const auto kern = hla_out_tc_kernel<DKP, DVP>;
-        constexpr size_t bytes = TileSmem<DKP>::bytes;
+        constexpr size_t bytes = OutTile<DKP>::bytes;
         if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
         kern<<<units * (DVP / 64), 256, bytes, a.stream>>>(m.q, m.k, m.v, t);
         return cudaGetLastError();
     }
-    if (a.dg) {
-        t.dots = reinterpret_cast<float *>(ws + l.dots);
-        t.through = reinterpret_cast<float *>(ws + l.through);
-    }
     const auto kern = hla_grad_tc_kernel<DKP, DVP>;
-    constexpr size_t b0 = TileSmem<DKP>::bytes, b1 = TileSmem<DVP>::bytes, bytes = b0 > b1 ? b0 : b1;
+    constexpr size_t bytes = GradTile<DKP, DVP>::bytes;
     if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
-    kern<<<units * (2 * (DKP / 64) + DVP / 64), 256, bytes, a.stream>>>(m.q, m.k, m.v, m.o, t);
-    if ((e = cudaGetLastError()) != cudaSuccess || !a.dg) return e;
-    hla_dg_tc_kernel<<<(units + 3) / 4, 128, 0, a.stream>>>(t, DKP / 64, units);
+    kern<<<units, 512, bytes, a.stream>>>(m.q, m.k, m.v, m.o, m.dq, m.dk, m.dv, t);
     return cudaGetLastError();
 }
 
@@ -715,7 +917,7 @@ cudaError_t pass(const HlaArgs &a, bool back) {
 
 bool hla_tc_supported(const HlaArgs &a) {
     // one tile per (chunk slot, head, slice of a result), in a 31-bit grid
-    return a.dtype == KDA_DTYPE_BF16 && hla_slots(a.cu_seqlens != nullptr, a.N, a.T, C) <= 0x7fffffffLL / 6 / a.H;
+    return a.dtype == KDA_DTYPE_BF16 && hla_slots(a.cu_seqlens != nullptr, a.N, a.T, C) <= 0x7fffffffLL / 2 / a.H;
 }
 size_t hla_tc_workspace(const HlaArgs &a, bool back) { return layout(a, back).bytes; }
 cudaError_t launch_hla_forward_tc(const HlaArgs &a) { return pass(a, false); }
