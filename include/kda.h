@@ -477,7 +477,7 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
  *            cores; bf16 only, else KDA_ERR_UNSUPPORTED). AUTO takes the tensor
  *            cores for bf16.
  *
- * Arithmetic: sums, states and decays in fp32 (the decays' sums in fp64). The
+ * Arithmetic: sums, states and decays in fp32 (the decays' sums in 64 bits). The
  * tensor cores take the scores and the states as bf16 operands; the states
  * themselves are carried in fp32, to about 2^-18.
  *

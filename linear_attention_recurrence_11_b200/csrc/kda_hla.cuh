@@ -15,10 +15,10 @@
 //          + sum_{s < t} e^{G_C - G_s} k_s.(R v_s) + e^{G_C} <S_in, R>
 // (every term of dg is a pair of a write before t and a read from t on: nothing cancels).
 //
-// The decays are differences of cumulative sums. The sums are taken in fp64 and kept as the sum
-// of two floats, so that a difference of two nearby large values (strong decays earlier in the
-// chunk) keeps its own precision: D_rs = 2^{(hi_r - hi_s) + (lo_r - lo_s)}. A g below kMinLog2
-// in units of log2 (-infinity among them) counts as kMinLog2: 2^-200 is zero in fp32.
+// The decays are differences of cumulative sums. The sums are exact (integers of 2^-40) and kept as
+// the sum of two floats, so that a difference of two nearby large values (strong decays earlier in
+// the chunk) keeps its own precision: D_rs = 2^{(hi_r - hi_s) + (lo_r - lo_s)}. A g below -kMaxLog2
+// in units of log2 (-infinity among them) counts as -kMaxLog2: 2^-200 is zero in fp32.
 #pragma once
 
 #include "kda_internal.cuh"
@@ -100,7 +100,7 @@ __device__ __forceinline__ bool hla_chunk_of(const HlaArgs &p, long long slot, i
 }
 
 constexpr double kLog2eD = 1.4426950408889634;
-constexpr double kMinLog2 = -200.0;
+constexpr double kMaxLog2 = 200.0;
 
 __device__ __forceinline__ float hla_ex2(float x) {
     float y;
@@ -110,39 +110,72 @@ __device__ __forceinline__ float hla_ex2(float x) {
 // 2^(a - b) for sums kept as two floats
 __device__ __forceinline__ float hla_decay(float2 a, float2 b) { return hla_ex2((a.x - b.x) + (a.y - b.y)); }
 
-// Cumulative log2-decays of one chunk, by one warp: G[r] (r < C) as two floats each; rows from Lc on
-// decay by nothing, so that G[C - 1] is the whole chunk's. `row0` is the chunk's first token row.
+// One chunk's log-decays, read by one warp: lane l holds rows l E .. + E - 1 (E = C / 32); rows from Lc on
+// decay by nothing. `row0` is the chunk's first token row. A token's log-decays of all heads are neighbours, a
+// head's are H apart: E loads of 32 sectors each. They are issued together and converted only when they are
+// summed; one at a time, each behind its own bounds check, they took 5 us per chunk.
 template <typename Tin, int C>
-__device__ __forceinline__ void hla_scan_gate(const HlaArgs &p, long long row0, int h, int Lc, float2 *G) {
+struct HlaGate {
+    Tin raw[C / 32];
+    float head;
+    int Lc;
+    bool by_head;
+
+    __device__ __forceinline__ void load(const HlaArgs &p, long long row0, int h, int Lc_) {
+        Lc = Lc_;
+        by_head = p.gate == KDA_HLA_GATE_HEAD;
+        if (by_head) {
+            head = static_cast<const float *>(p.g)[h];
+        } else {
+#pragma unroll
+            for (int e = 0; e < C / 32; ++e) {
+                const int r = min((int)(threadIdx.x & 31) * (C / 32) + e, Lc - 1);
+                raw[e] = static_cast<const Tin *>(p.g)[(size_t)(row0 + r) * p.H + h];
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int e) const {
+        return (int)(threadIdx.x & 31) * (C / 32) + e >= Lc ? 0.f : by_head ? head : ld_elem(raw, e);
+    }
+};
+// Their cumulative sums G[r] (r < C) in units of log2, as two floats each, by the same warp. The sums are integers
+// of 2^-40: exact, and an addition of two instructions, where fp64 took 1 us per chunk of the chains' time. A NaN
+// makes every sum from its row on one.
+template <typename Tin, int C>
+__device__ __forceinline__ void hla_scan_gate(const HlaGate<Tin, C> &gate, float2 *G) {
     constexpr int E = C / 32;
     const int lane = threadIdx.x & 31;
-    double x[E];
+    long long x[E];
+    int first_nan = E;  // among this lane's rows
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int r = lane * E + e;
-        double gv = 0.0;
-        if (r < Lc) {
-            gv = p.gate == KDA_HLA_GATE_HEAD ? (double)static_cast<const float *>(p.g)[h]
-                                             : (double)ld_elem(static_cast<const Tin *>(p.g), (size_t)(row0 + r) * p.H + h);
-            gv *= kLog2eD;
-            if (gv < kMinLog2) gv = kMinLog2;  // not fmax: a NaN stays one
-        }
-        x[e] = gv + (e ? x[e - 1] : 0.0);
+        const float g = gate.at(e);
+        if (g != g && first_nan == E) first_nan = e;
+        const double t = fmin(fmax((double)g * kLog2eD, -kMaxLog2), kMaxLog2);
+        x[e] = __double2ll_rn(t * 1099511627776.0) + (e ? x[e - 1] : 0);
     }
-    double sum = x[E - 1];
+    long long sum = x[E - 1];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, off);
+        const long long y = __shfl_up_sync(0xffffffffu, sum, off);
         if (lane >= off) sum += y;
     }
-    double before = __shfl_up_sync(0xffffffffu, sum, 1);
-    if (lane == 0) before = 0.0;
+    const long long before = sum - x[E - 1];
+    const bool nan_before = (__ballot_sync(0xffffffffu, first_nan < E) & ((1u << lane) - 1u)) != 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const double t = before + x[e];
-        const float hi = (float)t;
-        G[lane * E + e] = make_float2(hi, (float)(t - (double)hi));
+        const long long t = before + x[e];
+        float hi = __ll2float_rn(t);                                 // 24 bits
+        const float lo = __ll2float_rn(t - __float2ll_rn(hi));       // the rest, exactly a difference of integers
+        if (nan_before || e >= first_nan) hi = __int_as_float(0x7fffffff);
+        G[lane * E + e] = make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);  // 2^-40
     }
+}
+template <typename Tin, int C>
+__device__ __forceinline__ void hla_load_scan_gate(const HlaArgs &p, long long row0, int h, int Lc, float2 *G) {
+    HlaGate<Tin, C> gate;
+    gate.load(p, row0, h, Lc);
+    hla_scan_gate(gate, G);
 }
 
 // Launchers (return cudaSuccess or the launch error).

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(NT) hla_state_simt_kernel(const HlaArgs p, flo
 #pragma unroll
             for (int cx = 0; cx < NC; ++cx) dst[(size_t)(j0 + 4 * warp + i) * DK + lane + 32 * cx] = x[i][cx];
         __syncthreads();  // the previous chunk's tiles are consumed
-        if (warp == 0) hla_scan_gate<Tin, C>(p, row0, h, Lc, G);
+        if (warp == 0) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
         load_tile<Tin, DK, DK>(sA, DK, kRev ? p.q : p.k, row0, p.H, h, 0, Lc);
         load_tile<Tin, DV, JB>(sB, JB, kRev ? p.dO : p.v, row0, p.H, h, j0, Lc);
         __syncthreads();
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const bool has_state = c > 0 || p.S0 != nullptr;
 
-    if (threadIdx.x < 32) hla_scan_gate<Tin, C>(p, row0, h, Lc, G);
+    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
     load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc, p.scale);
     load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float2 g0 = make_float2(0.f, 0.f);
 
-    if (threadIdx.x < 32) hla_scan_gate<Tin, C>(p, row0, h, Lc, G);
+    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
     load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc);
     load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);

@@ -48,20 +48,22 @@ struct StateArgs {
     bool ends;          // first pass over segments: from zero, only the end states
 };
 
-// One CTA: all dv rows (the MMA's M) and 64 columns of dk. Thread: one row of X (a TMEM lane), whose
-// 64 columns it holds in registers; as a token it scales one row of a.
-template <int DVP>
+// One CTA of 256 threads per chain. Thread: half a row of X (a TMEM lane is a row of dv), DKP / 2 columns held in
+// registers; as a token it scales half a row of a. The operand tile of the incoming state is staged where the low
+// halves go next, and leaves by a bulk store while the chunk's tiles arrive.
+template <int DKP, int DVP>
 struct StateSmem {
-    static constexpr uint32_t B = 0, A = (DVP / 64) * TILE, LO = A + TILE, MISC = LO + TILE;
+    static constexpr uint32_t B = 0, A = (DVP / 64) * TILE, LO = A + (DKP / 64) * TILE, MISC = LO + (DKP / 64) * TILE;
     static constexpr uint32_t G = MISC + 64;                  // 2 x 128 float2
     static constexpr uint32_t bytes = G + 2 * C * 8 + 1024;   // slack for 1024-byte alignment
 };
 
 template <int DKP, int DVP>
-__global__ void __launch_bounds__(128) hla_state_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
-                                                           const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
-                                                           const StateArgs s, int dir0) {
-    using L = StateSmem<DVP>;
+__global__ void __launch_bounds__(256, 2) hla_state_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
+                                                              const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
+                                                              const StateArgs s) {
+    using L = StateSmem<DKP, DVP>;
+    constexpr int NX = DKP / 2;  // columns of a thread
     const HlaArgs &p = s.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -70,8 +72,8 @@ __global__ void __launch_bounds__(128) hla_state_tc_kernel(const __grid_constant
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bar_tma + 2);
     float2 *G = reinterpret_cast<float2 *>(sm + L::G);
 
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int dir = blockIdx.z + dir0, slice = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, half = warp >> 2;
+    const int dir = blockIdx.z;
     const int h = blockIdx.x % p.H;
     const long long su = blockIdx.x / p.H;  // sequence, or segment slot
     int n = (int)su, sg = 0;
@@ -90,65 +92,102 @@ __global__ void __launch_bounds__(128) hla_state_tc_kernel(const __grid_constant
     if (start && !s.sc) start += sbase_n;
     float *end = s.ends ? s.seg[dir] + sbase_s : (!last ? nullptr : dir ? p.dS0 : p.ST);
     if (end && !s.ends) end += sbase_n;
+    const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
+    const int nc = c1 - c0;
 
-    const int row = tid, cols = min(64, p.dk - 64 * slice);  // this thread's row of X, and the columns that exist
-    const size_t row_off = (size_t)row * p.dk + 64 * slice;
-    float x[64];
+    const auto issue = [&](int i) {  // one thread: the tiles of chunk i, and the next ones' way into L2
+        const CUtensorMap *ta = dir ? &tm_a1 : &tm_a0, *tb = dir ? &tm_b1 : &tm_b0;
+        const int tok = (int)(sp.t0 + (long long)chunk(i) * C);
+        mbar_arrive_expect_tx(bar_tma, (DKP / 64 + DVP / 64) * TILE);
 #pragma unroll
-    for (int e = 0; e < 64; e += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (start && row < p.dv && e < cols) v = *reinterpret_cast<const float4 *>(start + row_off + e);
-        x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
-    }
-
+        for (int b = 0; b < DKP / 64; ++b) tma_load_3d(sm + L::A + b * TILE, ta, bar_tma, 64 * b, h, tok);
+#pragma unroll
+        for (int b = 0; b < DVP / 64; ++b) tma_load_3d(sm + L::B + b * TILE, tb, bar_tma, 64 * b, h, tok);
+        if (i + 1 < nc) {
+            const int next = (int)(sp.t0 + (long long)chunk(i + 1) * C);
+#pragma unroll
+            for (int b = 0; b < DKP / 64; ++b) tma_prefetch_l2_3d(ta, 64 * b, h, next);
+#pragma unroll
+            for (int b = 0; b < DVP / 64; ++b) tma_prefetch_l2_3d(tb, 64 * b, h, next);
+        }
+    };
     if (tid == 0) {
         mbar_init(bar_tma, 1);
         mbar_init(bar_mma, 1);
         fence_mbar_init();
+        fence_proxy_async_smem();
+        if (nc > 0) issue(0);
     }
     if (warp == 0) {
-        tmem_alloc(s_tmem, 64);
+        __syncwarp();
+        tmem_alloc(s_tmem, DKP);
         tmem_relinquish();
     }
-    const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
-    const auto scan = [&](int i) {
+    HlaGate<__nv_bfloat16, C> gate;  // warp 1: the next chunk's log-decays, read a chunk ahead
+    const auto load_gate = [&](int i) {
         const int c = chunk(i);
-        hla_scan_gate<__nv_bfloat16, C>(p, sp.t0 + (long long)c * C, h, min(C, sp.len - c * C), G + (i & 1) * C);
+        gate.load(p, sp.t0 + (long long)c * C, h, min(C, sp.len - c * C));
     };
-    if (c0 < c1 && warp == 1) scan(0);
+    if (nc > 0 && warp == 1) {
+        load_gate(0);
+        hla_scan_gate(gate, G);
+        if (nc > 1) load_gate(1);
+    }
+
+    const int row = 32 * quarter + lane, col = NX * half;  // this thread's row of X, and its first column
+    const size_t row_off = (size_t)row * p.dk + col;
+    float x[NX];
+#pragma unroll
+    for (int e = 0; e < NX; e += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (start && row < p.dv && col + e < p.dk) v = *reinterpret_cast<const float4 *>(start + row_off + e);
+        x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
+    }
+    tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const uint32_t tlane = (uint32_t)(32 * warp) << 16;
+    const uint32_t tlane = (uint32_t)(32 * quarter) << 16;
 
-    const auto issue = [&](int i) {  // one thread: the tiles of chunk i
-        const int tok = (int)(sp.t0 + (long long)chunk(i) * C);
-        mbar_arrive_expect_tx(bar_tma, (1 + DVP / 64) * TILE);
-        tma_load_3d(sm + L::A, dir ? &tm_a1 : &tm_a0, bar_tma, 64 * slice, h, tok);
-#pragma unroll
-        for (int b = 0; b < DVP / 64; ++b) tma_load_3d(sm + L::B + b * TILE, dir ? &tm_b1 : &tm_b0, bar_tma, 64 * b, h, tok);
-    };
-    const int nc = c1 - c0;
-    if (tid == 0 && nc > 0) issue(0);
-    constexpr uint32_t idesc = idesc_bf16_f32(128, 64, 1, 1);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, DKP, 1, 1);
+    // as a token: row `tok` of a, from its 16-byte piece `q0` of block `blk` on
+    const int tok = tid & 127, blk = DKP == 128 ? tid >> 7 : 0, q0 = DKP == 128 ? 0 : 4 * (tid >> 7);
     uint32_t ph = 0;
     bool aborted = false, tma_open = nc > 0, mma_open = false;
     float total = 1.f;  // decay over the segment
     for (int i = 0; i < nc; ++i) {
         const int c = chunk(i), Lc = min(C, sp.len - c * C);
         const bool more = i + 1 < nc;
-        const float2 g0 = make_float2(0.f, 0.f), gC = G[(i & 1) * C + C - 1], gt = G[(i & 1) * C + tid];
+        if (!s.ends) {  // the state that this chunk starts from
+            if (row < DVP) {
+#pragma unroll
+                for (int q = 0; q < NX / 8; ++q)
+                    *reinterpret_cast<uint4 *>(sm + L::LO + (col >> 6) * (DVP * 128) + sw128_offset(row, (col & 63) + 8 * q)) =
+                        make_uint4(pack_bf2(x[8 * q], x[8 * q + 1]), pack_bf2(x[8 * q + 2], x[8 * q + 3]),
+                                   pack_bf2(x[8 * q + 4], x[8 * q + 5]), pack_bf2(x[8 * q + 6], x[8 * q + 7]));
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (tid == 0) {
+                bulk_store(s.blob[dir] + ((size_t)(sp.slot + c) * p.H + h) * blob_bytes(DKP, DVP), sm + L::LO, DKP * DVP * 2);
+                bulk_commit();
+                bulk_wait_read_all();
+            }
+            __syncwarp();
+        }
+        const float2 g0 = make_float2(0.f, 0.f), gC = G[(i & 1) * C + C - 1], gt = G[(i & 1) * C + tok];
         const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(gC, gt), keep = hla_decay(gC, g0);
         total *= keep;
         const bool ok_t = mbar_wait_bounded(bar_tma, ph, kWaitCycles);
         tma_open = !ok_t;
-        // row `tid` of a, times its weight, as hi + lo; a row behind the sequence's end is zero on both
-        // sides of the product (what stands there may be anything)
-        uint8_t *ra = sm + L::A, *rl = sm + L::LO;
-        if (tid < Lc) {
+        if (__syncthreads_or(!ok_t)) { aborted = true; break; }
+        // a row times its weight, as hi + lo; a row behind the sequence's end is zero on both sides of the
+        // product (what stands there may be anything)
+        uint8_t *ra = sm + L::A + blk * TILE, *rl = sm + L::LO + blk * TILE;
+        if (tok < Lc) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint32_t off = sw128_offset(tid, 8 * q);
+            for (int q = 0; q < NX / 8; ++q) {
+                const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
                 const uint4 v = *reinterpret_cast<const uint4 *>(ra + off);
                 const uint32_t in[4] = {v.x, v.y, v.z, v.w};
                 uint32_t hi[4], lo[4];
@@ -164,33 +203,32 @@ __global__ void __launch_bounds__(128) hla_state_tc_kernel(const __grid_constant
         } else {
             const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint32_t off = sw128_offset(tid, 8 * q);
+            for (int q = 0; q < NX / 8; ++q) {
+                const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
                 *reinterpret_cast<uint4 *>(ra + off) = z;
                 *reinterpret_cast<uint4 *>(rl + off) = z;
-#pragma unroll
-                for (int b = 0; b < DVP / 64; ++b) *reinterpret_cast<uint4 *>(sm + L::B + b * TILE + off) = z;
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int b = 0; b < DVP / 64; ++b)
+                    *reinterpret_cast<uint4 *>(sm + L::B + b * TILE + sw128_offset(tok, 8 * (4 * (tid >> 7) + q))) = z;
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        if (__syncthreads_or(!ok_t)) { aborted = true; break; }
+        __syncthreads();
         if (tid == 0) {  // (a 64-row dv is read twice as the upper half of M: lanes that nothing reads)
             tc_fence_after();
             const Opnd Ab{sbase + L::B, true, 0, DVP == 128 ? TILE : 0u};
-            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::A, true, 0, 0}, idesc, false);
-            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::LO, true, 0, 0}, idesc, true);
+            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::A, true, 0, TILE}, idesc, false);
+            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::LO, true, 0, TILE}, idesc, true);
             mma_commit(bar_mma);
         }
-        if (!s.ends && row < DVP) {  // the state that this chunk starts from
-            uint8_t *dst = s.blob[dir] + ((size_t)(sp.slot + c) * p.H + h) * blob_bytes(DKP, DVP) + (size_t)slice * DVP * 128;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<uint4 *>(dst + sw128_offset(row, 8 * q)) =
-                    make_uint4(pack_bf2(x[8 * q], x[8 * q + 1]), pack_bf2(x[8 * q + 2], x[8 * q + 3]),
-                               pack_bf2(x[8 * q + 4], x[8 * q + 5]), pack_bf2(x[8 * q + 6], x[8 * q + 7]));
+        __syncwarp();
+        if (more && warp == 1) {
+            hla_scan_gate(gate, G + ((i + 1) & 1) * C);
+            if (i + 2 < nc) load_gate(i + 2);
         }
-        if (more && warp == 1) scan(i + 1);
         const bool ok_m = mbar_wait_bounded(bar_mma, ph, kWaitCycles);
         mma_open = !ok_m;
         ph ^= 1u;
@@ -200,10 +238,11 @@ __global__ void __launch_bounds__(128) hla_state_tc_kernel(const __grid_constant
                 issue(i + 1);
                 tma_open = true;
             }
+            __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < NX / 16; ++q) {
                 float d[16];
-                tmem_ld16(tmem + tlane + 16u * q, d);
+                tmem_ld16(tmem + tlane + col + 16u * q, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[16 * q + e] = fmaf(keep, x[16 * q + e], d[e]);
@@ -221,23 +260,25 @@ __global__ void __launch_bounds__(128) hla_state_tc_kernel(const __grid_constant
         }
     } else if (end && row < p.dv) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 4)
-            if (e < cols) *reinterpret_cast<float4 *>(end + row_off + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        if (s.ends && tid == 0 && slice == 0) s.seg_keep[dir][su * p.H + h] = total;
+        for (int e = 0; e < NX; e += 4)
+            if (col + e < p.dk) *reinterpret_cast<float4 *>(end + row_off + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        if (s.ends && tid == 0) s.seg_keep[dir][su * p.H + h] = total;
     }
+    if (tid == 0) bulk_wait_all();
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 64);
+        tmem_dealloc(tmem, DKP);
     }
 }
 
 // End states of the segments -> their start states: start_0 = S0, start_{i+1} = keep_i start_i + end_i (in the
 // direction's order), in place, one thread per four elements of a (sequence, head).
-__global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s, int dir0) {
+__global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s) {
+    constexpr int U = 8;  // end states on their way at once
     const HlaArgs &p = s.a;
-    const int dir = blockIdx.z + dir0, h = blockIdx.x % p.H, n = blockIdx.x / p.H;
+    const int dir = blockIdx.z, h = blockIdx.x % p.H, n = blockIdx.x / p.H;
     const int at = 4 * (blockIdx.y * 256 + threadIdx.x), size = p.dv * p.dk;
     if (at >= size) return;
     const HlaSpan sp = hla_span(p, n, s.sc * C);
@@ -245,16 +286,22 @@ __global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s
     const float *first = dir ? p.dST : p.S0;
     float4 x = first ? *reinterpret_cast<const float4 *>(first + ((size_t)n * p.H + h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
     const auto where = [&](int i) { return (size_t)(sp.slot + (dir ? nseg - 1 - i : i)) * p.H + h; };
-    for (int i = 0; i < nseg; ++i) {
-        float4 *y = reinterpret_cast<float4 *>(s.seg[dir] + where(i) * size + at);
-        float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
-        float keep = 0.f;
-        if (i + 1 < nseg) {
-            e = *y;
-            keep = s.seg_keep[dir][where(i)];
-        }
-        *y = x;
-        x = make_float4(fmaf(keep, x.x, e.x), fmaf(keep, x.y, e.y), fmaf(keep, x.z, e.z), fmaf(keep, x.w, e.w));
+    for (int i0 = 0; i0 < nseg; i0 += U) {
+        float4 e[U];
+        float keep[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i0 + j + 1 < nseg) {  // (the last segment's end is the sequence's: it has no slot)
+                e[j] = *reinterpret_cast<const float4 *>(s.seg[dir] + where(i0 + j) * size + at);
+                keep[j] = s.seg_keep[dir][where(i0 + j)];
+            }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i0 + j < nseg) {
+                *reinterpret_cast<float4 *>(s.seg[dir] + where(i0 + j) * size + at) = x;
+                if (i0 + j + 1 < nseg)
+                    x = make_float4(fmaf(keep[j], x.x, e[j].x), fmaf(keep[j], x.y, e[j].y), fmaf(keep[j], x.z, e[j].z), fmaf(keep[j], x.w, e[j].w));
+            }
     }
 }
 
@@ -262,6 +309,7 @@ __global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s
 struct TileArgs {
     HlaArgs a;
     const uint8_t *S, *R;   // the chunks' incoming states, and the gradients of their outgoing ones
+    unsigned ahead;         // CTAs that run at once: the tile this many further on is prefetched into L2
 };
 
 // ------------------------------------------------------------------ outputs
@@ -325,7 +373,7 @@ __global__ void __launch_bounds__(256, 2) hla_out_tc_kernel(const __grid_constan
         tmem_alloc(s_tmem, 256);
         tmem_relinquish();
     }
-    if (warp == 1) hla_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
+    if (warp == 1) hla_load_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -443,7 +491,7 @@ struct GradTile {
     static constexpr bool over = DKP == 128 && DVP == 128;
     static constexpr uint32_t Q = 0, K = QB, V = 2 * QB, O = V + VB, S = O + VB, R = S + SB;
     static constexpr uint32_t A = over ? S : R + SB, dA = over ? V : A + 2 * TILE, END = over ? R + SB : dA + 2 * TILE;
-    static constexpr uint32_t G = END + 128, RED = G + C * 8;          // RED: 3 x 4 x 128 floats, and 16
+    static constexpr uint32_t G = END + 128, F = G + C * 8, RED = F + C * 4;   // RED: 3 x 4 x 128 floats, and 16
     static constexpr uint32_t bytes = RED + 12 * C * 4 + 64 + 1024;
     static_assert(bytes <= 232448, "shared memory budget");
 };
@@ -468,6 +516,7 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
     enum { L_QK, L_VO, L_SR, B_P, B_DP, B_SR, B_KR, B_QK, B_V, NBAR };
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + NBAR);
     float2 *G = reinterpret_cast<float2 *>(sm + L::G);
+    float *F = reinterpret_cast<float *>(sm + L::F);    // 2^{G_e - G_s}, e the last of the 32 columns that s is among
     float *red = reinterpret_cast<float *>(sm + L::RED);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, grp = warp >> 2;
@@ -495,13 +544,38 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         const size_t at = ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP);
         if (hasS) bulk_load(sm + L::S, t.S + at, L::SB, bars + L_SR);
         if (hasR) bulk_load(sm + L::R, t.R + at, L::SB, bars + L_SR);
+        // the tile that comes to this SM next (one CTA per SM) starts on its way from HBM now
+        const unsigned nb = blockIdx.x + t.ahead;
+        int n2, c2;
+        HlaSpan s2;
+        if (nb < gridDim.x && hla_chunk_of(p, nb / p.H, C, n2, c2, s2)) {
+            const int h2 = nb % p.H, row2 = (int)(s2.t0 + (long long)c2 * C);
+            const size_t at2 = ((size_t)(nb / p.H) * p.H + h2) * blob_bytes(DKP, DVP);
+#pragma unroll
+            for (int b = 0; b < DKP / 64; ++b) {
+                tma_prefetch_l2_3d(&tm_q, 64 * b, h2, row2);
+                tma_prefetch_l2_3d(&tm_k, 64 * b, h2, row2);
+            }
+#pragma unroll
+            for (int b = 0; b < DVP / 64; ++b) {
+                tma_prefetch_l2_3d(&tm_v, 64 * b, h2, row2);
+                tma_prefetch_l2_3d(&tm_o, 64 * b, h2, row2);
+            }
+            bulk_prefetch_l2(t.S + at2, L::SB);
+            bulk_prefetch_l2(t.R + at2, L::SB);
+        }
     }
     if (warp == 0) {
         __syncwarp();
         tmem_alloc(s_tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 1) hla_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
+    if (warp == 1) {
+        hla_load_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
+        __syncwarp();
+#pragma unroll
+        for (int s = lane; s < C; s += 32) F[s] = hla_decay(G[s | 31], G[s]);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -572,9 +646,30 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
     wait(B_P);
     wait(B_DP);
     tc_fence_after();
-    if (col > 32 * quarter + 31) {
+    if (col > 32 * quarter) {  // (32 columns, all behind these 32 rows)
 #pragma unroll
         for (int e = 0; e < 16; ++e) wa[e] = wd[e] = 0u;
+    } else if (ok && col < 32 * quarter) {
+        // all columns before these rows: D_rs = 2^{G_r - G_e} 2^{G_e - G_s}, e the last of the columns. Both factors are
+        // at most 1, and the second is the same for all rows: a product replaces the exponential (0.4 of the instructions)
+        const float x = r < Lc ? p.scale * hla_decay(gr, G[col + 31]) : 0.f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float a[16], d[16];
+            tmem_ld16(tmem + tlane + T0 + col + 16u * q, a);
+            tmem_ld16(tmem + tlane + T1 + col + 16u * q, d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(F + col + 16 * q + e);
+                const float y[4] = {x * f.x, x * f.y, x * f.z, x * f.w};
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    wa[8 * q + (e + k) / 2] = pack_bf2(y[k] * a[e + k], y[k + 1] * a[e + k + 1]);
+                    wd[8 * q + (e + k) / 2] = pack_bf2(y[k] * d[e + k], y[k + 1] * d[e + k + 1]);
+                }
+            }
+        }
     } else if (ok) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -767,7 +862,7 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
             bulk_commit();
         }
     }
-    if (tid == 0) bulk_wait_all();
+    if (tid == 0) bulk_wait_read_all();
     tc_fence_before();
     if (bad && tid == 0) {  // leave nothing in flight behind: the copies, and whatever products were issued
         if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
@@ -801,15 +896,16 @@ bool make_tile_map(CUtensorMap *m, const void *base, size_t tokens, int H, int d
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Chunks per segment (0: whole sequences). The chains run one after another; where there are too few of them to
-// fill the GPU (three CTAs per SM), sequences are cut into segments that run side by side, at the price of a first
+// fill the GPU (two CTAs per SM), sequences are cut into segments that run side by side, at the price of a first
 // pass for their end states.
 int segment_chunks(const HlaArgs &a, int dirs) {
-    const long long chains = (long long)a.N * a.H * (padded(a.dk) / 64) * dirs, want = 3LL * device_sm_count();
+    const long long chains = (long long)a.N * a.H * dirs, want = 2LL * device_sm_count();
     const long long chunks = a.cu_seqlens ? (long long)a.T / C + 1 : ((long long)a.T + C - 1) / C;  // of the longest sequence, at most
-    if (chains * 2 > want || chunks < 16) return 0;
-    const long long total = chunks * (a.cu_seqlens ? 1 : a.N) * (chains / a.N);
-    const long long sc = (total + want - 1) / want;
-    return (int)(sc < 4 ? 4 : sc);
+    if (chains * 3 > want || chunks < 8) return 0;
+    const long long total = a.cu_seqlens ? chunks * a.H * dirs : chunks * chains;
+    long long sc = (total + want - 1) / want;
+    if (!a.cu_seqlens) sc = (chunks + want / chains - 1) / (want / chains);  // equal parts
+    return (int)(sc < 2 ? 2 : sc);
 }
 
 struct Layout {
@@ -848,20 +944,20 @@ template <int DKP, int DVP>
 cudaError_t states(const StateArgs &s0, const Maps &m, const Layout &l, int dirs) {
     const HlaArgs &a = s0.a;
     const auto kern = hla_state_tc_kernel<DKP, DVP>;
-    constexpr size_t bytes = StateSmem<DVP>::bytes;
+    constexpr size_t bytes = StateSmem<DKP, DVP>::bytes;
     cudaError_t e = with_smem(kern, bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), DKP / 64, dirs);
+    const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), 1, dirs);
     StateArgs s = s0;
     if (l.sc) {
         s.ends = true;
-        kern<<<grid, 128, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s, 0);
+        kern<<<grid, 256, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        hla_segment_scan_kernel<<<dim3((unsigned)(a.N * a.H), (a.dk * a.dv + 1023) / 1024, dirs), 256, 0, a.stream>>>(s, 0);
+        hla_segment_scan_kernel<<<dim3((unsigned)(a.N * a.H), (a.dk * a.dv + 1023) / 1024, dirs), 256, 0, a.stream>>>(s);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         s.ends = false;
     }
-    kern<<<grid, 128, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s, 0);
+    kern<<<grid, 256, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s);
     return cudaGetLastError();
 }
 
@@ -900,6 +996,7 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
         kern<<<units * (DVP / 64), 256, bytes, a.stream>>>(m.q, m.k, m.v, t);
         return cudaGetLastError();
     }
+    t.ahead = device_sm_count();
     const auto kern = hla_grad_tc_kernel<DKP, DVP>;
     constexpr size_t bytes = GradTile<DKP, DVP>::bytes;
     if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;

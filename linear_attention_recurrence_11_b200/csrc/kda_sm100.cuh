@@ -93,6 +93,11 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *gmem_src, 
                  : "memory");
 }
 
+// Prefetch of `bytes` contiguous bytes into L2 (16-byte aligned, a multiple of 16; nothing to wait for).
+__device__ __forceinline__ void bulk_prefetch_l2(const void *gmem_src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gmem_src), "r"(bytes) : "memory");
+}
+
 // Bulk copy (no tensor map) of `bytes` contiguous bytes from shared to global memory,
 // completing through the bulk-group mechanism (bulk_commit / bulk_wait_*). Both addresses
 // 16-byte aligned, bytes a multiple of 16.
