@@ -110,6 +110,16 @@ __device__ __forceinline__ float hla_ex2(float x) {
 // 2^(a - b) for sums kept as two floats
 __device__ __forceinline__ float hla_decay(float2 a, float2 b) { return hla_ex2((a.x - b.x) + (a.y - b.y)); }
 
+// A log-decay in units of log2 as an integer of 2^-40, and a sum of them as two floats.
+__device__ __forceinline__ long long hla_gate_fixed(float g) {
+    return __double2ll_rn(fmin(fmax((double)g * kLog2eD, -kMaxLog2), kMaxLog2) * 1099511627776.0);
+}
+__device__ __forceinline__ float2 hla_gate_split(long long t) {
+    const float hi = __ll2float_rn(t);                        // 24 bits
+    const float lo = __ll2float_rn(t - __float2ll_rn(hi));    // the rest: a difference of integers
+    return make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);  // 2^-40
+}
+
 // One chunk's log-decays, read by one warp: lane l holds rows l E .. + E - 1 (E = C / 32); rows from Lc on
 // decay by nothing. `row0` is the chunk's first token row. A token's log-decays of all heads are neighbours, a
 // head's are H apart: E loads of 32 sectors each. They are issued together and converted only when they are
@@ -151,8 +161,7 @@ __device__ __forceinline__ void hla_scan_gate(const HlaGate<Tin, C> &gate, float
     for (int e = 0; e < E; ++e) {
         const float g = gate.at(e);
         if (g != g && first_nan == E) first_nan = e;
-        const double t = fmin(fmax((double)g * kLog2eD, -kMaxLog2), kMaxLog2);
-        x[e] = __double2ll_rn(t * 1099511627776.0) + (e ? x[e - 1] : 0);
+        x[e] = hla_gate_fixed(g) + (e ? x[e - 1] : 0);
     }
     long long sum = x[E - 1];
 #pragma unroll
@@ -164,11 +173,9 @@ __device__ __forceinline__ void hla_scan_gate(const HlaGate<Tin, C> &gate, float
     const bool nan_before = (__ballot_sync(0xffffffffu, first_nan < E) & ((1u << lane) - 1u)) != 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const long long t = before + x[e];
-        float hi = __ll2float_rn(t);                                 // 24 bits
-        const float lo = __ll2float_rn(t - __float2ll_rn(hi));       // the rest, exactly a difference of integers
-        if (nan_before || e >= first_nan) hi = __int_as_float(0x7fffffff);
-        G[lane * E + e] = make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);  // 2^-40
+        float2 t = hla_gate_split(before + x[e]);
+        if (nan_before || e >= first_nan) t.x = __int_as_float(0x7fffffff);
+        G[lane * E + e] = t;
     }
 }
 template <typename Tin, int C>

@@ -35,45 +35,163 @@ __host__ __device__ inline size_t blob_bytes(int dkp, int dvp) { return (size_t)
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// ================================================================= states
-// Direction 0: the state; a = k, b = v, row weights e^{G_C - G_s}, chunks in order, from S0 to S_T.
-// Direction 1: its gradient; a = q, b = dO, row weights scale e^{G_r}, chunks from the last to the
-// first, from dS_T to dS0. Per chunk X <- e^{G_C} X + b^T (w a), X [dv][dk].
-struct StateArgs {
+// =================================================================== gates
+// Of every (chunk slot, head), once for all kernels: the cumulative log2-decays G[128] as two floats each, and the
+// factors F[s] = 2^{G_e - G_s}, e the last of the 32 tokens that s is among (1.5 KB). A block takes 32 heads, whose
+// log-decays of a token are neighbours, and 16 tokens per thread.
+constexpr uint32_t GATE = C * 8 + C * 4;
+
+__global__ void __launch_bounds__(256) hla_gate_kernel(const HlaArgs p, uint8_t *__restrict__ gates) {
+    constexpr int E = 16, SEGS = C / E;
+    __shared__ long long tot[SEGS][32];
+    __shared__ float2 ends[SEGS][32];
+    __shared__ int nans[SEGS][32];
+    const long long slot = blockIdx.x;
+    const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5, h = blockIdx.y * 32 + lane;
+    int n, c;
+    HlaSpan sp;
+    if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
+    const int Lc = min(C, sp.len - c * C);
+    const size_t row0 = (size_t)(sp.t0 + (long long)c * C);
+    const int hh = min(h, p.H - 1);
+    float g[E];
+    if (p.gate == KDA_HLA_GATE_HEAD) {
+        const float x = static_cast<const float *>(p.g)[hh];
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] = x;
+    } else {
+        __nv_bfloat16 raw[E];  // (read together: one wait for all)
+#pragma unroll
+        for (int e = 0; e < E; ++e) raw[e] = static_cast<const __nv_bfloat16 *>(p.g)[(row0 + min(seg * E + e, Lc - 1)) * p.H + hh];
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] = __bfloat162float(raw[e]);
+    }
+    long long x[E];
+    int first_nan = E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float v = seg * E + e < Lc ? g[e] : 0.f;
+        if (v != v && first_nan == E) first_nan = e;
+        x[e] = hla_gate_fixed(v) + (e ? x[e - 1] : 0);
+    }
+    tot[seg][lane] = x[E - 1];
+    nans[seg][lane] = first_nan < E;
+    __syncthreads();
+    long long before = 0;
+    bool nan_before = false;
+#pragma unroll
+    for (int k = 0; k < SEGS; ++k)
+        if (k < seg) {
+            before += tot[k][lane];
+            nan_before |= nans[k][lane] != 0;
+        }
+    float2 G[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        G[e] = hla_gate_split(before + x[e]);
+        if (nan_before || e >= first_nan) G[e].x = __int_as_float(0x7fffffff);
+    }
+    ends[seg][lane] = G[E - 1];
+    __syncthreads();
+    if (h >= p.H) return;
+    const float2 ge = ends[seg | 1][lane];
+    uint8_t *dst = gates + ((size_t)slot * p.H + h) * GATE;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<float4 *>(dst + (seg * E + e) * 8) = make_float4(G[e].x, G[e].y, G[e + 1].x, G[e + 1].y);
+#pragma unroll
+    for (int e = 0; e < E; e += 4)
+        *reinterpret_cast<float4 *>(dst + C * 8 + (seg * E + e) * 4) =
+            make_float4(hla_decay(ge, G[e]), hla_decay(ge, G[e + 1]), hla_decay(ge, G[e + 2]), hla_decay(ge, G[e + 3]));
+}
+
+// Masked decayed scores of one TMEM row r (in the 32 rows from R on) and the 32 columns from `col` on, in bf16 pairs:
+// x D_rs, D_rs = 2^{G_r - G_s} for s <= r, and 0 above. Columns that all come before these rows take D_rs as
+// 2^{G_r - G_e} F_s, e the last of the columns: both factors are at most 1, the second is the same for all rows, and a
+// product replaces the exponential (5 instructions an element instead of 12).
+struct DecayRow {
+    const float2 *G;
+    const float *F;
+    float2 gr;
+    int r, R, Lc;
+    float scale;
+    // the decays of columns col + 16 q .. + 15, times scale; zero where masked
+    __device__ __forceinline__ bool none(int col) const { return col > R; }
+    __device__ __forceinline__ void get(int col, int q, float (&d)[16]) const {
+        if (col < R) {
+            const float x = r < Lc ? scale * hla_decay(gr, G[col + 31]) : 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(F + col + 16 * q + e);
+                d[e] = x * f.x; d[e + 1] = x * f.y; d[e + 2] = x * f.z; d[e + 3] = x * f.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int s = col + 16 * q + e;
+                d[e] = s <= r && r < Lc ? scale * hla_decay(gr, G[s]) : 0.f;
+            }
+        }
+    }
+    // x d with the masked elements dropped, not multiplied: they may be anything
+    __device__ __forceinline__ float keep(int s, float x, float d) const { return s <= r && r < Lc ? x * d : 0.f; }
+};
+
+// ================================================================== chains
+// The chunks of a sequence (or of a segment of it), one after the other, by one CTA per chain.
+//   kOut:    the outputs; the state stays in the SM from chunk to chunk.
+//   kStates: each chunk's incoming state as an operand tile for the gradients (or, dir 1, the gradient of its
+//            outgoing state, from the last chunk to the first).
+//   kEnds:   a segment's end state, from zero.
+// Per chunk X <- e^{G_C} X + b^T (w a), X [dv][dk] fp32 in registers; direction 0: a = k, b = v, w = e^{G_C - G_s}, from S0
+// to S_T; direction 1: a = q, b = dO, w = scale e^{G_r}, from dS_T to dS0. The increment does not depend on X, so only
+// the two instructions per element of that update are serial; everything else is pipelined over the chunks:
+//   warps 0-7    scale a into hi + lo; decay and mask the scores into bf16 (in TMEM)
+//   warps 8-15   the state: update, operand copy; the outputs: rows of Q S scaled, result stored
+//   warp 16      issues the products: Q K^T; b^T hi + b^T lo; Q S; (scores) V onto the scaled Q S
+//   warp 17      the copies: a tile is requested again as soon as the last product that reads it is done
+enum { kOut = 0, kStates = 1, kEnds = 2 };
+
+struct ChainArgs {
     HlaArgs a;
-    uint8_t *blob[2];   // per direction: chunk operands [slot][H]
+    const uint8_t *gates;
+    uint8_t *blob[2];   // kStates, per direction: chunk operands [slot][H]
     float *seg[2];      // per direction: states of the segments [segment slot][H][dv][dk]
     float *seg_keep[2]; // per direction: decay over each segment [segment slot][H]
     int sc;             // chunks per segment; 0: whole sequences
-    bool ends;          // first pass over segments: from zero, only the end states
+    const int32_t *order;  // packed batches: sequences, longest first (null: as they come)
 };
 
-// One CTA of 256 threads per chain. Thread: half a row of X (a TMEM lane is a row of dv), DKP / 2 columns held in
-// registers; as a token it scales half a row of a. The operand tile of the incoming state is staged where the low
-// halves go next, and leaves by a bulk store while the chunk's tiles arrive.
-template <int DKP, int DVP>
-struct StateSmem {
-    static constexpr uint32_t B = 0, A = (DVP / 64) * TILE, LO = A + (DKP / 64) * TILE, MISC = LO + (DKP / 64) * TILE;
-    static constexpr uint32_t G = MISC + 64;                  // 2 x 128 float2
-    static constexpr uint32_t bytes = G + 2 * C * 8 + 1024;   // slack for 1024-byte alignment
+template <int DKP, int DVP, int kMode>
+struct ChainSmem {
+    static constexpr uint32_t KB_ = (DKP / 64) * TILE, VB = (DVP / 64) * TILE;
+    static constexpr uint32_t K = 0, HI = KB_, LO = 2 * KB_, V = 3 * KB_, S = V + VB, Q = S + DKP * DVP * 2;
+    static constexpr uint32_t G = Q + (kMode == kOut ? KB_ : 0u), BARS = G + 4 * GATE;  // a ring of four chunks' gates
+    static constexpr uint32_t bytes = BARS + 256 + 1024;  // slack for 1024-byte alignment
+    static_assert(bytes <= 232448, "shared memory budget");
 };
 
-template <int DKP, int DVP>
-__global__ void __launch_bounds__(256, 2) hla_state_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
-                                                              const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
-                                                              const StateArgs s) {
-    using L = StateSmem<DKP, DVP>;
-    constexpr int NX = DKP / 2;  // columns of a thread
+template <int DKP, int DVP, int kMode>
+__global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                                                              const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
+                                                              const ChainArgs s) {
+    using L = ChainSmem<DKP, DVP, kMode>;
+    constexpr int NX = DKP / 2, NO = DVP / 2;  // columns of a thread: of X, of the outputs
     const HlaArgs &p = s.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
-    uint64_t *bar_tma = reinterpret_cast<uint64_t *>(sm + L::MISC), *bar_mma = bar_tma + 1;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bar_tma + 2);
-    float2 *G = reinterpret_cast<float2 *>(sm + L::G);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
+    // every barrier completes once per chunk: its phase is the chunk's parity
+    enum { F_K, F_Q, F_V,                    // tiles have arrived (K's with the gates)
+           D_SCALE, D_P, D_X, D_S, D_O, D_E,  // done: hi + lo; scores; increment read; operand; Q S scaled; outputs read
+           C_QK, C_X, C_QS, C_PV, C_END,     // products
+           R_S = F_Q,                         // kStates: the operand tile has been read by its store
+           NBAR = C_END + 1 };
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + NBAR);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, half = warp >> 2;
-    const int dir = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int dir = kMode == kOut ? 0 : blockIdx.z;
     const int h = blockIdx.x % p.H;
     const long long su = blockIdx.x / p.H;  // sequence, or segment slot
     int n = (int)su, sg = 0;
@@ -81,201 +199,339 @@ __global__ void __launch_bounds__(256, 2) hla_state_tc_kernel(const __grid_const
     if (s.sc) {
         hla_chunk_of(p, su, s.sc * C, n, sg, sp);
         if (sg < 0 || sg >= max(1, sp.nch)) return;  // (an empty sequence keeps one segment, which passes its state on)
+    } else if (s.order) {
+        n = s.order[n];
     }
     sp = hla_span(p, n, C);
     const int nseg = s.sc ? max(1, (sp.nch + s.sc - 1) / s.sc) : 1;
-    const int c0 = s.sc ? sg * s.sc : 0, c1 = s.sc ? min(sp.nch, c0 + s.sc) : sp.nch;
+    const int c0 = s.sc ? sg * s.sc : 0, c1 = s.sc ? min(sp.nch, c0 + s.sc) : sp.nch, nc = c1 - c0;
     const bool last = dir ? sg == 0 : sg == nseg - 1;  // the segment whose end is the sequence's
-    if (s.ends && last) return;
-    const size_t sbase_n = ((size_t)n * p.H + h) * (size_t)(p.dv * p.dk), sbase_s = ((size_t)su * p.H + h) * (size_t)(p.dv * p.dk);
-    const float *start = s.ends ? nullptr : s.sc ? s.seg[dir] + sbase_s : dir ? p.dST : p.S0;
-    if (start && !s.sc) start += sbase_n;
-    float *end = s.ends ? s.seg[dir] + sbase_s : (!last ? nullptr : dir ? p.dS0 : p.ST);
-    if (end && !s.ends) end += sbase_n;
+    if (kMode == kEnds && last) return;
+    const size_t base_n = ((size_t)n * p.H + h) * (size_t)(p.dv * p.dk), base_s = ((size_t)su * p.H + h) * (size_t)(p.dv * p.dk);
+    const float *start = kMode == kEnds ? nullptr : s.sc ? s.seg[dir] + base_s : dir ? p.dST : p.S0;
+    if (start && !s.sc) start += base_n;
+    float *end = kMode == kEnds ? s.seg[dir] + base_s : (!last ? nullptr : dir ? p.dS0 : p.ST);
+    if (end && kMode != kEnds) end += base_n;
     const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
-    const int nc = c1 - c0;
+    const auto rows_of = [&](int i) { return min(C, sp.len - chunk(i) * C); };
+    const auto row_of = [&](int i) { return sp.t0 + (long long)chunk(i) * C; };
+    const auto G = [&](int i) { return reinterpret_cast<const float2 *>(sm + L::G + (i & 3) * GATE); };
+    const float2 g0 = make_float2(0.f, 0.f);
 
-    const auto issue = [&](int i) {  // one thread: the tiles of chunk i, and the next ones' way into L2
-        const CUtensorMap *ta = dir ? &tm_a1 : &tm_a0, *tb = dir ? &tm_b1 : &tm_b0;
-        const int tok = (int)(sp.t0 + (long long)chunk(i) * C);
-        mbar_arrive_expect_tx(bar_tma, (DKP / 64 + DVP / 64) * TILE);
-#pragma unroll
-        for (int b = 0; b < DKP / 64; ++b) tma_load_3d(sm + L::A + b * TILE, ta, bar_tma, 64 * b, h, tok);
-#pragma unroll
-        for (int b = 0; b < DVP / 64; ++b) tma_load_3d(sm + L::B + b * TILE, tb, bar_tma, 64 * b, h, tok);
-        if (i + 1 < nc) {
-            const int next = (int)(sp.t0 + (long long)chunk(i + 1) * C);
-#pragma unroll
-            for (int b = 0; b < DKP / 64; ++b) tma_prefetch_l2_3d(ta, 64 * b, h, next);
-#pragma unroll
-            for (int b = 0; b < DVP / 64; ++b) tma_prefetch_l2_3d(tb, 64 * b, h, next);
-        }
-    };
     if (tid == 0) {
-        mbar_init(bar_tma, 1);
-        mbar_init(bar_mma, 1);
+        for (int i = 0; i < NBAR; ++i) mbar_init(bars + i, i >= D_SCALE && i <= D_E ? 8 : 1);
         fence_mbar_init();
         fence_proxy_async_smem();
-        if (nc > 0) issue(0);
     }
-    if (warp == 0) {
-        __syncwarp();
-        tmem_alloc(s_tmem, DKP);
+    if (warp == 16) {
+        tmem_alloc(s_tmem, kMode == kOut ? 512 : 128);
         tmem_relinquish();
-    }
-    HlaGate<__nv_bfloat16, C> gate;  // warp 1: the next chunk's log-decays, read a chunk ahead
-    const auto load_gate = [&](int i) {
-        const int c = chunk(i);
-        gate.load(p, sp.t0 + (long long)c * C, h, min(C, sp.len - c * C));
-    };
-    if (nc > 0 && warp == 1) {
-        load_gate(0);
-        hla_scan_gate(gate, G);
-        if (nc > 1) load_gate(1);
-    }
-
-    const int row = 32 * quarter + lane, col = NX * half;  // this thread's row of X, and its first column
-    const size_t row_off = (size_t)row * p.dk + col;
-    float x[NX];
-#pragma unroll
-    for (int e = 0; e < NX; e += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (start && row < p.dv && col + e < p.dk) v = *reinterpret_cast<const float4 *>(start + row_off + e);
-        x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const uint32_t tlane = (uint32_t)(32 * quarter) << 16;
+    constexpr uint32_t TX = 0, TO = 128, TS = 256, TP = 384;  // increment, outputs, scores, bf16 scores
 
-    constexpr uint32_t idesc = idesc_bf16_f32(128, DKP, 1, 1);
-    // as a token: row `tok` of a, from its 16-byte piece `q0` of block `blk` on
-    const int tok = tid & 127, blk = DKP == 128 ? tid >> 7 : 0, q0 = DKP == 128 ? 0 : 4 * (tid >> 7);
-    uint32_t ph = 0;
-    bool aborted = false, tma_open = nc > 0, mma_open = false;
-    float total = 1.f;  // decay over the segment
-    for (int i = 0; i < nc; ++i) {
-        const int c = chunk(i), Lc = min(C, sp.len - c * C);
-        const bool more = i + 1 < nc;
-        if (!s.ends) {  // the state that this chunk starts from
-            if (row < DVP) {
+    bool ok = true;
+    const auto wait = [&](int b, int i) {
+        if (ok) ok = mbar_wait_bounded(bars + b, (uint32_t)i & 1u, kWaitCycles);
+        return ok;
+    };
+    // a warp's threads have done their part: their writes to shared memory and TMEM are seen by what waits on b
+    const auto done = [&](int b) {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + b);
+    };
+
+    if (warp < 8) {
+        // ---------------------------------------------------- operands
+        const int quarter = warp & 3, half = warp >> 2, R = 32 * quarter, r = R + lane;
+        const uint32_t tlane = (uint32_t)R << 16;
+        // as a token: row `tok` of a, from its 16-byte piece `q0` of block `blk` on
+        const int tok = tid & 127, blk = DKP == 128 ? tid >> 7 : 0, q0 = DKP == 128 ? 0 : 4 * (tid >> 7);
+        for (int i = 0; i < nc && ok; ++i) {
+            const int Lc = rows_of(i);
+            wait(F_K, i);
+            if (Lc < C) wait(F_V, i);
+            if (i > 0) wait(C_X, i - 1);  // hi and lo are read
+            if (!ok) break;
+            // a row times its weight, as hi + lo; a row behind the sequence's end is zero on both sides of
+            // the products (what stands there may be anything)
+            const uint8_t *ra = sm + L::K + blk * TILE;
+            uint8_t *rh = sm + L::HI + blk * TILE, *rl = sm + L::LO + blk * TILE;
+            if (tok < Lc) {
+                const float2 gt = G(i)[tok];
+                const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(G(i)[C - 1], gt);
+#pragma unroll
+                for (int q = 0; q < NX / 8; ++q) {
+                    const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(ra + off);
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = w * bf_lo(in[e]), b = w * bf_hi(in[e]);
+                        hi[e] = pack_bf2(a, b);
+                        lo[e] = pack_bf2(a - bf_lo(hi[e]), b - bf_hi(hi[e]));
+                    }
+                    *reinterpret_cast<uint4 *>(rh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(rl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            } else {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < NX / 8; ++q) {
+                    const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
+                    *reinterpret_cast<uint4 *>(rh + off) = z;
+                    *reinterpret_cast<uint4 *>(rl + off) = z;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int b = 0; b < DVP / 64; ++b)
+                        *reinterpret_cast<uint4 *>(sm + L::V + b * TILE + sw128_offset(tok, 8 * (4 * (tid >> 7) + q))) = z;
+            }
+            done(D_SCALE);
+            if (kMode != kOut) continue;
+            wait(C_QK, i);
+            if (i > 0) wait(C_PV, i - 1);  // the bf16 scores are read
+            if (!ok) break;
+            tc_fence_after();
+            const DecayRow dr{G(i), reinterpret_cast<const float *>(G(i) + C), G(i)[r], r, R, Lc, p.scale};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int col = 64 * half + 32 * k;
+                float w[16];  // bf16 pairs
+                if (dr.none(col)) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = 0.f;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float v[16], d[16];
+                        tmem_ld16(tmem + tlane + TS + col + 16u * q, v);
+                        dr.get(col, q, d);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int c = col + 16 * q + 2 * e;
+                            w[8 * q + e] = __uint_as_float(pack_bf2(dr.keep(c, v[2 * e], d[2 * e]), dr.keep(c + 1, v[2 * e + 1], d[2 * e + 1])));
+                        }
+                    }
+                }
+                tmem_st16(tmem + tlane + TP + 32u * half + 16u * k, w);
+            }
+            tmem_wait_st();
+            done(D_P);
+        }
+    } else if (warp < 16) {
+        // ------------------------------------------------- state, outputs
+        const int quarter = warp & 3, half = (warp >> 2) & 1, r = 32 * quarter + lane, col = NX * half;
+        const uint32_t tlane = (uint32_t)(32 * quarter) << 16;
+        const size_t row_off = (size_t)r * p.dk + col;
+        float x[NX];  // row r of X (dv), columns from col on
+#pragma unroll
+        for (int e = 0; e < NX; e += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (start && r < p.dv && col + e < p.dk) v = *reinterpret_cast<const float4 *>(start + row_off + e);
+            x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
+        }
+        const auto operand = [&]() {  // X in bf16, as a K-major tile of dv rows
+            if (r < DVP) {
 #pragma unroll
                 for (int q = 0; q < NX / 8; ++q)
-                    *reinterpret_cast<uint4 *>(sm + L::LO + (col >> 6) * (DVP * 128) + sw128_offset(row, (col & 63) + 8 * q)) =
+                    *reinterpret_cast<uint4 *>(sm + L::S + (col >> 6) * (DVP * 128) + sw128_offset(r, (col & 63) + 8 * q)) =
                         make_uint4(pack_bf2(x[8 * q], x[8 * q + 1]), pack_bf2(x[8 * q + 2], x[8 * q + 3]),
                                    pack_bf2(x[8 * q + 4], x[8 * q + 5]), pack_bf2(x[8 * q + 6], x[8 * q + 7]));
             }
-            fence_proxy_async_smem();
-            __syncthreads();
-            if (tid == 0) {
-                bulk_store(s.blob[dir] + ((size_t)(sp.slot + c) * p.H + h) * blob_bytes(DKP, DVP), sm + L::LO, DKP * DVP * 2);
-                bulk_commit();
-                bulk_wait_read_all();
-            }
-            __syncwarp();
+        };
+        if (kMode == kOut && nc > 0) {
+            operand();
+            done(D_S);
         }
-        const float2 g0 = make_float2(0.f, 0.f), gC = G[(i & 1) * C + C - 1], gt = G[(i & 1) * C + tok];
-        const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(gC, gt), keep = hla_decay(gC, g0);
-        total *= keep;
-        const bool ok_t = mbar_wait_bounded(bar_tma, ph, kWaitCycles);
-        tma_open = !ok_t;
-        if (__syncthreads_or(!ok_t)) { aborted = true; break; }
-        // a row times its weight, as hi + lo; a row behind the sequence's end is zero on both sides of the
-        // product (what stands there may be anything)
-        uint8_t *ra = sm + L::A + blk * TILE, *rl = sm + L::LO + blk * TILE;
-        if (tok < Lc) {
-#pragma unroll
-            for (int q = 0; q < NX / 8; ++q) {
-                const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
-                const uint4 v = *reinterpret_cast<const uint4 *>(ra + off);
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = w * bf_lo(in[e]), b = w * bf_hi(in[e]);
-                    hi[e] = pack_bf2(a, b);
-                    lo[e] = pack_bf2(a - bf_lo(hi[e]), b - bf_hi(hi[e]));
+        float total = 1.f;  // decay over the chain
+        for (int i = 0; i < nc && ok; ++i) {
+            if (kMode == kStates) {
+                if (i > 0) {
+                    if (tid == 256) {
+                        bulk_wait_read_all();
+                        mbar_arrive(bars + R_S);
+                    }
+                    __syncwarp();
+                    if (!wait(R_S, i - 1)) break;
                 }
-                *reinterpret_cast<uint4 *>(ra + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(rl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                operand();
+                done(D_S);
+                if (tid == 256 && wait(D_S, i)) {
+                    bulk_store(s.blob[dir] + ((size_t)(sp.slot + chunk(i)) * p.H + h) * blob_bytes(DKP, DVP), sm + L::S, DKP * DVP * 2);
+                    bulk_commit();
+                }
+                __syncwarp();
             }
-        } else {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int q = 0; q < NX / 8; ++q) {
-                const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
-                *reinterpret_cast<uint4 *>(ra + off) = z;
-                *reinterpret_cast<uint4 *>(rl + off) = z;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int b = 0; b < DVP / 64; ++b)
-                    *reinterpret_cast<uint4 *>(sm + L::B + b * TILE + sw128_offset(tok, 8 * (4 * (tid >> 7) + q))) = z;
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {  // (a 64-row dv is read twice as the upper half of M: lanes that nothing reads)
+            wait(C_X, i);
+            if (!ok) break;
             tc_fence_after();
-            const Opnd Ab{sbase + L::B, true, 0, DVP == 128 ? TILE : 0u};
-            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::A, true, 0, TILE}, idesc, false);
-            mma_chain<C / 16>(tmem, Ab, Opnd{sbase + L::LO, true, 0, TILE}, idesc, true);
-            mma_commit(bar_mma);
-        }
-        __syncwarp();
-        if (more && warp == 1) {
-            hla_scan_gate(gate, G + ((i + 1) & 1) * C);
-            if (i + 2 < nc) load_gate(i + 2);
-        }
-        const bool ok_m = mbar_wait_bounded(bar_mma, ph, kWaitCycles);
-        mma_open = !ok_m;
-        ph ^= 1u;
-        tc_fence_after();
-        if (ok_m) {
-            if (more && tid == 0) {
-                issue(i + 1);
-                tma_open = true;
-            }
-            __syncwarp();
+            const float keep = hla_decay(G(i)[C - 1], g0);
+            total *= keep;
 #pragma unroll
             for (int q = 0; q < NX / 16; ++q) {
                 float d[16];
-                tmem_ld16(tmem + tlane + col + 16u * q, d);
+                tmem_ld16(tmem + tlane + TX + col + 16u * q, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[16 * q + e] = fmaf(keep, x[16 * q + e], d[e]);
             }
-        }
-        tc_fence_before();
-        if (__syncthreads_or(!ok_m)) { aborted = true; break; }
-    }
-    if (aborted) {  // leave nothing in flight behind (the waits are bounded again)
-        if (tid == 0) {
-            if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
-            // a copy that is open was issued for the phase after the one that the MMA wait flipped to
-            if (tma_open) mbar_wait_bounded(bar_tma, ph, kWaitCycles);
-            if (mma_open) mbar_wait_bounded(bar_mma, ph ^ 1u, kWaitCycles);
-        }
-    } else if (end && row < p.dv) {
+            done(D_X);
+            if (kMode != kOut) continue;
+            wait(C_QS, i);
+            if (!ok) break;
+            tc_fence_after();
+            const float since = p.scale * hla_decay(G(i)[r], g0);
+            const int oc = NO * half;
 #pragma unroll
-        for (int e = 0; e < NX; e += 4)
-            if (col + e < p.dk) *reinterpret_cast<float4 *>(end + row_off + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        if (s.ends && tid == 0) s.seg_keep[dir][su * p.H + h] = total;
+            for (int q = 0; q < NO / 16; ++q) {
+                float v[16];
+                tmem_ld16(tmem + tlane + TO + oc + 16u * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] *= since;
+                tmem_st16(tmem + tlane + TO + oc + 16u * q, v);
+            }
+            tmem_wait_st();
+            done(D_O);
+            if (i + 1 < nc) {
+                operand();
+                done(D_S);
+            }
+            wait(C_PV, i);
+            if (!ok) break;
+            tc_fence_after();
+            const int Lc = rows_of(i);
+            uint8_t *out = static_cast<uint8_t *>(p.o) + (((size_t)(row_of(i) + r) * p.H + h) * p.dv + oc) * 2;
+#pragma unroll
+            for (int q = 0; q < NO / 16; ++q) {
+                float v[16];
+                tmem_ld16(tmem + tlane + TO + oc + 16u * q, v);
+                tmem_wait_ld();
+                if (r < Lc && oc + 16 * q < p.dv) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(out + 32 * q);
+                    dst[0] = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
+                    dst[1] = make_uint4(pack_bf2(v[8], v[9]), pack_bf2(v[10], v[11]), pack_bf2(v[12], v[13]), pack_bf2(v[14], v[15]));
+                }
+            }
+            done(D_E);
+        }
+        if (ok && end && r < p.dv) {
+#pragma unroll
+            for (int e = 0; e < NX; e += 4)
+                if (col + e < p.dk) *reinterpret_cast<float4 *>(end + row_off + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        }
+        if (kMode == kEnds && ok && tid == 256) s.seg_keep[dir][su * p.H + h] = total;
+        if (kMode == kStates && tid == 256) bulk_wait_read_all();
+    } else if (warp == 16) {
+        // ----------------------------------------------------- products
+        if (lane == 0) {
+            const Opnd oQ{sbase + L::Q, false, TILE, 0}, oK{sbase + L::K, false, TILE, 0}, oS{sbase + L::S, false, DVP * 128, 0};
+            // (a 64-row dv is read twice as the upper half of M: lanes that nothing reads)
+            const Opnd oVt{sbase + L::V, true, 0, DVP == 128 ? TILE : 0u}, oHi{sbase + L::HI, true, 0, TILE}, oLo{sbase + L::LO, true, 0, TILE};
+            const uint64_t dV = smem_desc_sw128(sbase + L::V, TILE, 1024u);
+            constexpr uint32_t idX = idesc_bf16_f32(128, DKP, 1, 1), idS = idesc_bf16_f32(128, 128, 0, 0), idO = idesc_bf16_f32(128, DVP, 0, 0),
+                               idP = idesc_bf16_f32(128, DVP, 0, 1);
+            for (int i = 0; i < nc && ok; ++i) {
+                if (kMode == kOut) {
+                    wait(F_K, i);
+                    if (!wait(F_Q, i)) break;
+                    tc_fence_after();
+                    mma_chain<DKP / 16>(tmem + TS, oQ, oK, idS, false);  // (the scores before were read before D_P, waited for below)
+                    mma_commit(bars + C_QK);
+                }
+                wait(D_SCALE, i);
+                wait(F_V, i);
+                if (i > 0) wait(D_X, i - 1);
+                if (!ok) break;
+                tc_fence_after();
+                mma_chain<C / 16>(tmem + TX, oVt, oHi, idX, false);
+                mma_chain<C / 16>(tmem + TX, oVt, oLo, idX, true);
+                mma_commit(bars + C_X);
+                if (kMode == kOut) {
+                    wait(D_S, i);
+                    if (i > 0) wait(D_E, i - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_chain<DKP / 16>(tmem + TO, oQ, oS, idO, false);
+                    mma_commit(bars + C_QS);
+                    wait(D_P, i);
+                    wait(D_O, i);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k) mma_bf16_ts(tmem + TO, tmem + TP + 8u * k, dV + (uint64_t)((k * 2048u) >> 4), idP, 1u);
+                    mma_commit(bars + C_PV);
+                }
+            }
+            mma_commit(bars + C_END);  // nothing may be in flight when TMEM is freed
+            ok = mbar_wait_bounded(bars + C_END, 0, kWaitCycles) && ok;
+        }
+        __syncwarp();
+    } else if (lane == 0) {
+        // ------------------------------------------------------- copies
+        const CUtensorMap *ta = dir ? &tm_q : &tm_k, *tb = dir ? &tm_o : &tm_v;
+        int issued_k = 0, issued_q = 0, issued_v = 0;
+        for (int i = 0; i < nc && ok; ++i) {
+            const int tok = (int)row_of(i), next = i + 1 < nc ? (int)row_of(i + 1) : -1;
+            if (i > 0) {
+                wait(D_SCALE, i - 1);
+                if (kMode == kOut) wait(C_QK, i - 1);
+            }
+            // (the gates' ring: chunk i - 4's outputs are stored once chunk i - 1's scores are done, or its increment)
+            if (!ok) break;
+            mbar_arrive_expect_tx(bars + F_K, L::KB_ + GATE);
+            ++issued_k;
+            bulk_load(sm + L::G + (i & 3) * GATE, s.gates + ((size_t)(sp.slot + chunk(i)) * p.H + h) * GATE, GATE, bars + F_K);
+#pragma unroll
+            for (int b = 0; b < DKP / 64; ++b) {
+                tma_load_3d(sm + L::K + b * TILE, ta, bars + F_K, 64 * b, h, tok);
+                if (next >= 0) tma_prefetch_l2_3d(ta, 64 * b, h, next);
+            }
+            if (kMode == kOut) {
+                if (i > 0 && !wait(C_QS, i - 1)) break;
+                mbar_arrive_expect_tx(bars + F_Q, L::KB_);
+                ++issued_q;
+#pragma unroll
+                for (int b = 0; b < DKP / 64; ++b) {
+                    tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + F_Q, 64 * b, h, tok);
+                    if (next >= 0) tma_prefetch_l2_3d(&tm_q, 64 * b, h, next);
+                }
+            }
+            if (i > 0 && !wait(kMode == kOut ? C_PV : C_X, i - 1)) break;  // (products end in order)
+            mbar_arrive_expect_tx(bars + F_V, L::VB);
+            ++issued_v;
+#pragma unroll
+            for (int b = 0; b < DVP / 64; ++b) {
+                tma_load_3d(sm + L::V + b * TILE, tb, bars + F_V, 64 * b, h, tok);
+                if (next >= 0) tma_prefetch_l2_3d(tb, 64 * b, h, next);
+            }
+        }
+        // nothing may be in flight when the CTA ends: the last copies of each kind (bounded)
+        if (issued_k) mbar_wait_bounded(bars + F_K, (uint32_t)(issued_k - 1) & 1u, kWaitCycles);
+        if (issued_q) mbar_wait_bounded(bars + F_Q, (uint32_t)(issued_q - 1) & 1u, kWaitCycles);
+        if (issued_v) mbar_wait_bounded(bars + F_V, (uint32_t)(issued_v - 1) & 1u, kWaitCycles);
     }
-    if (tid == 0) bulk_wait_all();
+    if (!ok && p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 16) {
         tc_fence_after();
-        tmem_dealloc(tmem, DKP);
+        tmem_dealloc(tmem, kMode == kOut ? 512 : 128);
     }
 }
 
 // End states of the segments -> their start states: start_0 = S0, start_{i+1} = keep_i start_i + end_i (in the
 // direction's order), in place, one thread per four elements of a (sequence, head).
-__global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s) {
+__global__ void __launch_bounds__(256) hla_segment_scan_kernel(const ChainArgs s) {
     constexpr int U = 8;  // end states on their way at once
     const HlaArgs &p = s.a;
     const int dir = blockIdx.z, h = blockIdx.x % p.H, n = blockIdx.x / p.H;
@@ -305,179 +561,14 @@ __global__ void __launch_bounds__(256) hla_segment_scan_kernel(const StateArgs s
     }
 }
 
-// ================================================================== tiles
+// =============================================================== gradients
 struct TileArgs {
     HlaArgs a;
+    const uint8_t *gates;
     const uint8_t *S, *R;   // the chunks' incoming states, and the gradients of their outgoing ones
     unsigned ahead;         // CTAs that run at once: the tile this many further on is prefetched into L2
 };
 
-// ------------------------------------------------------------------ outputs
-// O = scale [(Q K^T . D) V + e^{G_r} Q S]. One CTA per chunk, head and 64 columns of dv.
-template <int XD>
-struct OutTile {
-    static constexpr uint32_t X = 0, Y = (XD / 64) * TILE, P = XD == 128 ? Y : Y + TILE;  // the scores go over K where it has room
-    static constexpr uint32_t Z = P + 2 * TILE, W = Z + TILE, MISC = W + (XD / 64) * 8 * KB;
-    static constexpr uint32_t G = MISC + 64;
-    static constexpr uint32_t bytes = G + C * 8 + 1024;
-};
-
-template <int DKP, int DVP>
-__global__ void __launch_bounds__(256, 2) hla_out_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                                                            const __grid_constant__ CUtensorMap tm_v, const TileArgs t) {
-    using L = OutTile<DKP>;
-    const HlaArgs &p = t.a;
-    constexpr int parts = DVP / 64;
-    const int z = blockIdx.x % parts;
-    const unsigned u = blockIdx.x / parts;
-    const long long slot = u / p.H;
-    const int h = u % p.H;
-    int n, c;
-    HlaSpan sp;
-    if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t sbase = smem_u32(sm);
-    uint64_t *bar_xy = reinterpret_cast<uint64_t *>(sm + L::MISC), *bar_zw = bar_xy + 1, *bar_s = bar_xy + 2, *bar_o = bar_xy + 3;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bar_xy + 4);
-    float2 *G = reinterpret_cast<float2 *>(sm + L::G);
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, half = warp >> 2;
-    const long long row0 = sp.t0 + (long long)c * C;
-    const int Lc = min(C, sp.len - c * C);
-    const bool has = p.S0 != nullptr || c > 0;  // a state that is not all zeros
-
-    if (tid == 0) {
-        mbar_init(bar_xy, 1);
-        mbar_init(bar_zw, 1);
-        mbar_init(bar_s, 1);
-        mbar_init(bar_o, 1);
-        fence_mbar_init();
-        fence_proxy_async_smem();
-        mbar_arrive_expect_tx(bar_xy, 2 * (DKP / 64) * TILE);
-#pragma unroll
-        for (int b = 0; b < DKP / 64; ++b) {
-            tma_load_3d(sm + L::X + b * TILE, &tm_q, bar_xy, 64 * b, h, (int)row0);
-            tma_load_3d(sm + L::Y + b * TILE, &tm_k, bar_xy, 64 * b, h, (int)row0);
-        }
-        mbar_arrive_expect_tx(bar_zw, TILE + (has ? (DKP / 64) * 8 * KB : 0u));
-        tma_load_3d(sm + L::Z, &tm_v, bar_zw, 64 * z, h, (int)row0);
-        if (has) {  // rows 64 z .. + 63 of every block of 64 dk
-            const uint8_t *src = t.S + ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP) + (size_t)z * 8 * KB;
-#pragma unroll
-            for (int b = 0; b < DKP / 64; ++b) bulk_load(sm + L::W + b * 8 * KB, src + (size_t)b * DVP * 128, 8 * KB, bar_zw);
-        }
-    }
-    if (warp == 0) {
-        __syncwarp();
-        tmem_alloc(s_tmem, 256);
-        tmem_relinquish();
-    }
-    if (warp == 1) hla_load_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem, tlane = (uint32_t)(32 * quarter) << 16;
-    constexpr uint32_t TS = 0, T1 = 128, T2 = 192;  // scores, (scores) V, Q S
-
-    bool ok = true;
-    if (tid == 0) {
-        ok = mbar_wait_bounded(bar_xy, 0, kWaitCycles);
-        if (ok) {
-            mma_chain<DKP / 16>(tmem + TS, Opnd{sbase + L::X, false, TILE, 0}, Opnd{sbase + L::Y, false, TILE, 0},
-                                idesc_bf16_f32(128, 128, 0, 0), false);
-            mma_commit(bar_s);
-        }
-    }
-    __syncwarp();
-    const bool ok_zw = mbar_wait_bounded(bar_zw, 0, kWaitCycles);
-    if (tid == 0 && ok && ok_zw && has)
-        mma_chain<DKP / 16>(tmem + T2, Opnd{sbase + L::X, false, TILE, 0}, Opnd{sbase + L::W, false, 8 * KB, 0},
-                            idesc_bf16_f32(128, 64, 0, 0), false);
-    if (Lc < C && ok_zw) {  // rows of V behind the sequence's end: zero, whatever stands there
-        for (int i = tid; i < (C - Lc) * 8; i += 256)
-            *reinterpret_cast<uint4 *>(sm + L::Z + sw128_offset(Lc + (i >> 3), 8 * (i & 7))) = make_uint4(0, 0, 0, 0);
-    }
-    __syncwarp();
-    const bool ok_s = mbar_wait_bounded(bar_s, 0, kWaitCycles);
-    tc_fence_after();
-
-    // scores -> decayed, masked, bf16: the K-major operand of the second product
-    const int r = 32 * quarter + lane;
-    const float2 gr = G[r];
-    if (ok_s) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int s0 = 64 * half + 16 * q;
-            uint32_t w[8];
-            if (s0 > 32 * quarter + 31) {  // 32 rows and 16 columns that the mask leaves nothing of
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = 0u;
-            } else {
-                float v[16];
-                tmem_ld16(tmem + tlane + TS + s0, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = s0 + e <= r ? v[e] * hla_decay(gr, G[s0 + e]) : 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = pack_bf2(v[2 * e], v[2 * e + 1]);
-            }
-            uint8_t *dst = sm + L::P + half * TILE;
-            *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 16 * q)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 16 * q + 8)) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    const bool bad = __syncthreads_or(!ok || !ok_zw || !ok_s);
-    bool ok_o = false;
-    if (!bad) {
-        if (tid == 0) {
-            tc_fence_after();
-            mma_chain<C / 16>(tmem + T1, Opnd{sbase + L::P, false, TILE, 0}, Opnd{sbase + L::Z, true, 0, 0},
-                              idesc_bf16_f32(128, 64, 0, 1), false);
-            mma_commit(bar_o);
-        }
-        __syncwarp();
-        ok_o = mbar_wait_bounded(bar_o, 0, kWaitCycles);
-        tc_fence_after();
-    }
-    if (ok_o) {
-        const float c2 = p.scale * hla_decay(gr, make_float2(0.f, 0.f));
-        const int col = 64 * z + 32 * half;
-        const size_t at = ((size_t)(row0 + r) * p.H + h) * p.dv + col;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float v1[16], v2[16];
-            tmem_ld16(tmem + tlane + T1 + 32u * half + 16u * q, v1);
-            if (has) tmem_ld16(tmem + tlane + T2 + 32u * half + 16u * q, v2);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v1[e] = has ? fmaf(p.scale, v1[e], c2 * v2[e]) : p.scale * v1[e];
-            if (r < Lc && col < p.dv) {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at + 16 * q);
-                dst[0] = make_uint4(pack_bf2(v1[0], v1[1]), pack_bf2(v1[2], v1[3]), pack_bf2(v1[4], v1[5]), pack_bf2(v1[6], v1[7]));
-                dst[1] = make_uint4(pack_bf2(v1[8], v1[9]), pack_bf2(v1[10], v1[11]), pack_bf2(v1[12], v1[13]), pack_bf2(v1[14], v1[15]));
-            }
-        }
-    }
-    tc_fence_before();
-    const bool failed = __syncthreads_or(!ok_o);
-    if (failed && tid == 0) {  // leave nothing in flight behind
-        if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
-        mbar_wait_bounded(bar_xy, 0, kWaitCycles);
-        mbar_wait_bounded(bar_zw, 0, kWaitCycles);
-        mma_commit(bad ? bar_o : bar_s);  // whatever products were issued (bar_s and bar_o count one arrival each)
-        mbar_wait_bounded(bad ? bar_o : bar_s, bad ? 0u : 1u, kWaitCycles);
-    }
-    __syncthreads();
-    if (warp == 0) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 256);
-    }
-}
-
-// ---------------------------------------------------------------- gradients
 // All gradients of a (chunk, head), by one CTA of 512 threads. With P = Q K^T and dP = dO V^T (both [row r, column
 // s], so that one decay D_rs serves both), A = scale P . D and dA = scale dP . D in bf16:
 //   dQ = dA K   + scale e^{G_r} dO S      accumulators T2
@@ -491,7 +582,7 @@ struct GradTile {
     static constexpr bool over = DKP == 128 && DVP == 128;
     static constexpr uint32_t Q = 0, K = QB, V = 2 * QB, O = V + VB, S = O + VB, R = S + SB;
     static constexpr uint32_t A = over ? S : R + SB, dA = over ? V : A + 2 * TILE, END = over ? R + SB : dA + 2 * TILE;
-    static constexpr uint32_t G = END + 128, F = G + C * 8, RED = F + C * 4;   // RED: 3 x 4 x 128 floats, and 16
+    static constexpr uint32_t G = END + 128, RED = G + GATE;   // RED: 3 x 4 x 128 floats, and 16
     static constexpr uint32_t bytes = RED + 12 * C * 4 + 64 + 1024;
     static_assert(bytes <= 232448, "shared memory budget");
 };
@@ -515,8 +606,7 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::END);
     enum { L_QK, L_VO, L_SR, B_P, B_DP, B_SR, B_KR, B_QK, B_V, NBAR };
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + NBAR);
-    float2 *G = reinterpret_cast<float2 *>(sm + L::G);
-    float *F = reinterpret_cast<float *>(sm + L::F);    // 2^{G_e - G_s}, e the last of the 32 columns that s is among
+    const float2 *G = reinterpret_cast<const float2 *>(sm + L::G);
     float *red = reinterpret_cast<float *>(sm + L::RED);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, grp = warp >> 2;
@@ -528,7 +618,8 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         for (int i = 0; i < NBAR; ++i) mbar_init(bars + i, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(bars + L_QK, 2 * L::QB);
+        mbar_arrive_expect_tx(bars + L_QK, 2 * L::QB + GATE);
+        bulk_load(sm + L::G, t.gates + ((size_t)slot * p.H + h) * GATE, GATE, bars + L_QK);
 #pragma unroll
         for (int b = 0; b < DKP / 64; ++b) {
             tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + L_QK, 64 * b, h, (int)row0);
@@ -570,19 +661,13 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         tmem_alloc(s_tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 1) {
-        hla_load_scan_gate<__nv_bfloat16, C>(p, row0, h, Lc, G);
-        __syncwarp();
-#pragma unroll
-        for (int s = lane; s < C; s += 32) F[s] = hla_decay(G[s | 31], G[s]);
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem, tlane = (uint32_t)(32 * quarter) << 16;
     constexpr uint32_t T0 = 0, T1 = 128, T2 = 256, T3 = 384;
     const int r = 32 * quarter + lane, col = 32 * grp;   // this thread's row, and its 32 columns
-    const float2 g0 = make_float2(0.f, 0.f), gr = G[r];
+    const float2 g0 = make_float2(0.f, 0.f);
     const auto zero16 = [&](uint32_t off) { *reinterpret_cast<uint4 *>(sm + off) = make_uint4(0, 0, 0, 0); };
 
     bool ok = true;
@@ -646,49 +731,25 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
     wait(B_P);
     wait(B_DP);
     tc_fence_after();
-    if (col > 32 * quarter) {  // (32 columns, all behind these 32 rows)
+    wait(L_QK);  // (the gates came with q and k)
+    const float2 gr = G[r];
+    const DecayRow dr{G, reinterpret_cast<const float *>(G + C), gr, r, 32 * quarter, Lc, p.scale};
+    if (dr.none(col)) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) wa[e] = wd[e] = 0u;
-    } else if (ok && col < 32 * quarter) {
-        // all columns before these rows: D_rs = 2^{G_r - G_e} 2^{G_e - G_s}, e the last of the columns. Both factors are
-        // at most 1, and the second is the same for all rows: a product replaces the exponential (0.4 of the instructions)
-        const float x = r < Lc ? p.scale * hla_decay(gr, G[col + 31]) : 0.f;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float a[16], d[16];
-            tmem_ld16(tmem + tlane + T0 + col + 16u * q, a);
-            tmem_ld16(tmem + tlane + T1 + col + 16u * q, d);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(F + col + 16 * q + e);
-                const float y[4] = {x * f.x, x * f.y, x * f.z, x * f.w};
-#pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    wa[8 * q + (e + k) / 2] = pack_bf2(y[k] * a[e + k], y[k + 1] * a[e + k + 1]);
-                    wd[8 * q + (e + k) / 2] = pack_bf2(y[k] * d[e + k], y[k + 1] * d[e + k + 1]);
-                }
-            }
-        }
     } else if (ok) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            float a[16], d[16];
+            float a[16], d[16], f[16];
             tmem_ld16(tmem + tlane + T0 + col + 16u * q, a);
             tmem_ld16(tmem + tlane + T1 + col + 16u * q, d);
+            dr.get(col, q, f);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int s = col + 16 * q + e;
-                const float x = p.scale * hla_decay(gr, G[s]);
-                const bool in = s <= r && r < Lc;
-                a[e] = in ? a[e] * x : 0.f;
-                d[e] = in ? d[e] * x : 0.f;
-            }
-#pragma unroll
             for (int e = 0; e < 8; ++e) {
-                wa[8 * q + e] = pack_bf2(a[2 * e], a[2 * e + 1]);
-                wd[8 * q + e] = pack_bf2(d[2 * e], d[2 * e + 1]);
+                const int c = col + 16 * q + 2 * e;
+                wa[8 * q + e] = pack_bf2(dr.keep(c, a[2 * e], f[2 * e]), dr.keep(c + 1, a[2 * e + 1], f[2 * e + 1]));
+                wd[8 * q + e] = pack_bf2(dr.keep(c, d[2 * e], f[2 * e]), dr.keep(c + 1, d[2 * e + 1], f[2 * e + 1]));
             }
         }
     }
@@ -895,23 +956,23 @@ bool make_tile_map(CUtensorMap *m, const void *base, size_t tokens, int H, int d
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Chunks per segment (0: whole sequences). The chains run one after another; where there are too few of them to
-// fill the GPU (two CTAs per SM), sequences are cut into segments that run side by side, at the price of a first
-// pass for their end states.
+// Chunks per segment (0: whole sequences). A chain's chunks run one after another; where there are too few chains to
+// fill the GPU (one CTA per SM), sequences are cut into segments that run side by side, at the price of a pass
+// for their end states, a scan over those, and two launches: as long as half a dozen chunks.
 int segment_chunks(const HlaArgs &a, int dirs) {
-    const long long chains = (long long)a.N * a.H * dirs, want = 2LL * device_sm_count();
-    const long long chunks = a.cu_seqlens ? (long long)a.T / C + 1 : ((long long)a.T + C - 1) / C;  // of the longest sequence, at most
-    if (chains * 3 > want || chunks < 8) return 0;
-    const long long total = a.cu_seqlens ? chunks * a.H * dirs : chunks * chains;
-    long long sc = (total + want - 1) / want;
-    if (!a.cu_seqlens) sc = (chunks + want / chains - 1) / (want / chains);  // equal parts
-    return (int)(sc < 2 ? 2 : sc);
+    const long long chains = (long long)a.N * a.H * dirs, sms = device_sm_count();
+    const long long chunks = a.cu_seqlens ? ((long long)a.T + C - 1) / C : ((long long)a.T + C - 1) / C;  // of the longest sequence, at most
+    const long long parts = sms / chains;  // of each sequence
+    if (parts < 2) return 0;
+    const long long sc = (chunks + parts - 1) / parts;
+    return 2 * sc + 6 < chunks ? (int)sc : 0;
 }
 
 struct Layout {
     int sc;
+    bool order;
     long long slots, seg_slots;
-    size_t blob[2], seg[2], keep[2], bytes;
+    size_t order_at, gates, blob[2], seg[2], keep[2], bytes;
 };
 Layout layout(const HlaArgs &a, bool back) {
     Layout l{};
@@ -922,8 +983,12 @@ Layout layout(const HlaArgs &a, bool back) {
     l.seg_slots = l.sc ? hla_slots(packed, a.N, a.T, l.sc * C) : 0;
     size_t at = 0;
     const auto take = [&](size_t bytes) { const size_t x = at; at += align256(bytes); return x; };
+    // more chains than SMs, of different lengths: the longest first
+    l.order = packed && !l.sc && seq_order_bytes(a.N) > 0 && (long long)a.N * a.H * dirs > device_sm_count();
+    l.order_at = take(l.order ? seq_order_bytes(a.N) : 0);
+    l.gates = take((size_t)l.slots * a.H * GATE);
     for (int d = 0; d < dirs; ++d) {
-        l.blob[d] = take((size_t)l.slots * a.H * blob_bytes(dkp, dvp));
+        l.blob[d] = take(back ? (size_t)l.slots * a.H * blob_bytes(dkp, dvp) : 0);
         l.seg[d] = take((size_t)l.seg_slots * a.H * a.dk * a.dv * 4);
         l.keep[d] = take((size_t)l.seg_slots * a.H * 4);
     }
@@ -931,33 +996,17 @@ Layout layout(const HlaArgs &a, bool back) {
     return l;
 }
 
-template <typename F>
-cudaError_t with_smem(F kern, size_t bytes) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 struct Maps {
     CUtensorMap q, k, v, o, dq, dk, dv;
 };
 
-template <int DKP, int DVP>
-cudaError_t states(const StateArgs &s0, const Maps &m, const Layout &l, int dirs) {
-    const HlaArgs &a = s0.a;
-    const auto kern = hla_state_tc_kernel<DKP, DVP>;
-    constexpr size_t bytes = StateSmem<DKP, DVP>::bytes;
-    cudaError_t e = with_smem(kern, bytes);
+template <int DKP, int DVP, int kMode>
+cudaError_t chain(const ChainArgs &s, const Maps &m, const Layout &l, int dirs) {
+    const auto kern = hla_chain_tc_kernel<DKP, DVP, kMode>;
+    constexpr size_t bytes = ChainSmem<DKP, DVP, kMode>::bytes;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), 1, dirs);
-    StateArgs s = s0;
-    if (l.sc) {
-        s.ends = true;
-        kern<<<grid, 256, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        hla_segment_scan_kernel<<<dim3((unsigned)(a.N * a.H), (a.dk * a.dv + 1023) / 1024, dirs), 256, 0, a.stream>>>(s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        s.ends = false;
-    }
-    kern<<<grid, 256, bytes, a.stream>>>(m.k, m.v, m.q, m.o, s);
+    kern<<<dim3((unsigned)((l.sc ? l.seg_slots : s.a.N) * s.a.H), 1, dirs), 576, bytes, s.a.stream>>>(m.k, m.v, m.q, m.o, s);
     return cudaGetLastError();
 }
 
@@ -972,34 +1021,43 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
                  !make_tile_map(&m.dv, a.dv_, tokens, a.H, a.dv)))
         return cudaErrorInvalidValue;
     const Layout l = layout(a, back);
+    const int dirs = back ? 2 : 1;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
-    StateArgs s{};
+    ChainArgs s{};
     s.a = a;
     if (back) s.a.ST = nullptr;
     s.sc = l.sc;
-    for (int d = 0; d < (back ? 2 : 1); ++d) {
+    s.gates = ws + l.gates;
+    for (int d = 0; d < dirs; ++d) {
         s.blob[d] = ws + l.blob[d];
         s.seg[d] = reinterpret_cast<float *>(ws + l.seg[d]);
         s.seg_keep[d] = reinterpret_cast<float *>(ws + l.keep[d]);
     }
-    cudaError_t e = states<DKP, DVP>(s, m, l, back ? 2 : 1);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    if (l.order) {
+        int32_t *order = reinterpret_cast<int32_t *>(ws + l.order_at);
+        if ((e = launch_seq_order(a.cu_seqlens, a.N, order, a.stream)) != cudaSuccess) return e;
+        s.order = order;
+    }
+    const unsigned units = (unsigned)(l.slots * a.H);
+    hla_gate_kernel<<<dim3((unsigned)l.slots, (a.H + 31) / 32), 256, 0, a.stream>>>(a, ws + l.gates);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (l.sc) {
+        if ((e = chain<DKP, DVP, kEnds>(s, m, l, dirs)) != cudaSuccess) return e;
+        hla_segment_scan_kernel<<<dim3((unsigned)(a.N * a.H), (a.dk * a.dv + 1023) / 1024, dirs), 256, 0, a.stream>>>(s);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (!back) return chain<DKP, DVP, kOut>(s, m, l, 1);
+    if ((e = chain<DKP, DVP, kStates>(s, m, l, 2)) != cudaSuccess) return e;
     TileArgs t{};
     t.a = a;
+    t.gates = s.gates;
     t.S = s.blob[0];
     t.R = s.blob[1];
-    const unsigned units = (unsigned)(l.slots * a.H);
-    if (!back) {
-        const auto kern = hla_out_tc_kernel<DKP, DVP>;
-        constexpr size_t bytes = OutTile<DKP>::bytes;
-        if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
-        kern<<<units * (DVP / 64), 256, bytes, a.stream>>>(m.q, m.k, m.v, t);
-        return cudaGetLastError();
-    }
     t.ahead = device_sm_count();
     const auto kern = hla_grad_tc_kernel<DKP, DVP>;
     constexpr size_t bytes = GradTile<DKP, DVP>::bytes;
-    if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) != cudaSuccess) return e;
     kern<<<units, 512, bytes, a.stream>>>(m.q, m.k, m.v, m.o, m.dq, m.dk, m.dv, t);
     return cudaGetLastError();
 }
