@@ -148,9 +148,11 @@ struct DecayRow {
 // the two instructions per element of that update are serial; everything else is pipelined over the chunks:
 //   warps 0-7    scale a into hi + lo; decay and mask the scores into bf16 (in TMEM)
 //   warps 8-15   the state: update, operand copy; the outputs: rows of Q S scaled, result stored
-//   warp 16      issues the products: Q K^T; b^T hi + b^T lo; Q S; (scores) V onto the scaled Q S
+//   warp 16      issues the products: Q K^T; Q S; b^T hi + b^T lo; (scores) V onto the scaled Q S
 //   warp 17      the copies: a tile is requested again as soon as the last product that reads it is done
 enum { kOut = 0, kStates = 1, kEnds = 2 };
+// 5 warpgroups launched at 96 registers a thread, 480 in all: two go down to 88, two up to 120, the last down to 64
+constexpr int kChainThreads = 640;
 
 struct ChainArgs {
     HlaArgs a;
@@ -162,19 +164,23 @@ struct ChainArgs {
     const int32_t *order;  // packed batches: sequences, longest first (null: as they come)
 };
 
+// Outputs: one tile each of a, its hi and lo halves, b, q, the state, and the outputs' staging. States: two of a, whose hi
+// halves replace it, and two of b.
 template <int DKP, int DVP, int kMode>
 struct ChainSmem {
-    static constexpr uint32_t KB_ = (DKP / 64) * TILE, VB = (DVP / 64) * TILE;
-    static constexpr uint32_t K = 0, HI = KB_, LO = 2 * KB_, V = 3 * KB_, S = V + VB, Q = S + DKP * DVP * 2;
-    static constexpr uint32_t G = Q + (kMode == kOut ? KB_ : 0u), BARS = G + 4 * GATE;  // a ring of four chunks' gates
-    static constexpr uint32_t bytes = BARS + 256 + 1024;  // slack for 1024-byte alignment
+    static constexpr bool out = kMode == kOut;
+    static constexpr uint32_t KT = (DKP / 64) * TILE, VT = (DVP / 64) * TILE;
+    static constexpr uint32_t K = 0, HI = out ? KT : 0u, LO = 2 * KT, V = 3 * KT, S = V + (out ? 1 : 2) * VT, Q = S + DKP * DVP * 2;
+    static constexpr uint32_t O = Q + (out ? KT : 0u);             // 8 warps x 32 rows of 32 columns
+    static constexpr uint32_t G = O + (out ? 16 * KB : 0u), BARS = G + 4 * GATE;  // a ring of four chunks' gates
+    static constexpr uint32_t bytes = BARS + 256 + 1024;           // slack for 1024-byte alignment
     static_assert(bytes <= 232448, "shared memory budget");
 };
 
 template <int DKP, int DVP, int kMode>
-__global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                                                              const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
-                                                              const ChainArgs s) {
+__global__ void __launch_bounds__(kChainThreads, 1)
+hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_o, const ChainArgs s) {
     using L = ChainSmem<DKP, DVP, kMode>;
     constexpr int NX = DKP / 2, NO = DVP / 2;  // columns of a thread: of X, of the outputs
     const HlaArgs &p = s.a;
@@ -183,8 +189,10 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
     const uint32_t sbase = smem_u32(sm);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
     // every barrier completes once per chunk: its phase is the chunk's parity
-    enum { F_K, F_Q, F_V,                    // tiles have arrived (K's with the gates)
-           D_SCALE, D_P, D_X, D_S, D_O, D_E,  // done: hi + lo; scores; increment read; operand; Q S scaled; outputs read
+    // (the loads': once per tile buffer, of which the states' kernels have two)
+    constexpr int NS = kMode == kOut ? 1 : 2;
+    enum { F_K, F_V = F_K + 2, F_Q = F_V + 2,  // tiles have arrived (a's with the gates)
+           D_SCALE = F_Q + 1, D_P, D_X, D_S, D_O, D_E,  // done: hi + lo; scores; increment read; operand; Q S scaled; outputs read
            C_QK, C_X, C_QS, C_PV, C_END,     // products
            R_S = F_Q,                         // kStates: the operand tile has been read by its store
            NBAR = C_END + 1 };
@@ -238,6 +246,7 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
         if (ok) ok = mbar_wait_bounded(bars + b, (uint32_t)i & 1u, kWaitCycles);
         return ok;
     };
+    const auto wait_tile = [&](int b, int i) { return NS == 1 ? wait(b, i) : wait(b + (i & 1), i >> 1); };
     // a warp's threads have done their part: their writes to shared memory and TMEM are seen by what waits on b
     const auto done = [&](int b) {
         fence_proxy_async_smem();
@@ -248,20 +257,22 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
 
     if (warp < 8) {
         // ---------------------------------------------------- operands
+        regs_dec<88>();
         const int quarter = warp & 3, half = warp >> 2, R = 32 * quarter, r = R + lane;
         const uint32_t tlane = (uint32_t)R << 16;
         // as a token: row `tok` of a, from its 16-byte piece `q0` of block `blk` on
         const int tok = tid & 127, blk = DKP == 128 ? tid >> 7 : 0, q0 = DKP == 128 ? 0 : 4 * (tid >> 7);
         for (int i = 0; i < nc && ok; ++i) {
             const int Lc = rows_of(i);
-            wait(F_K, i);
-            if (Lc < C) wait(F_V, i);
+            wait_tile(F_K, i);
+            if (Lc < C) wait_tile(F_V, i);
             if (i > 0) wait(C_X, i - 1);  // hi and lo are read
             if (!ok) break;
             // a row times its weight, as hi + lo; a row behind the sequence's end is zero on both sides of
             // the products (what stands there may be anything)
-            const uint8_t *ra = sm + L::K + blk * TILE;
-            uint8_t *rh = sm + L::HI + blk * TILE, *rl = sm + L::LO + blk * TILE;
+            const uint32_t kt = NS == 1 ? 0u : (i & 1) * L::KT;
+            const uint8_t *ra = sm + L::K + kt + blk * TILE;
+            uint8_t *rh = sm + L::HI + kt + blk * TILE, *rl = sm + L::LO + blk * TILE;
             if (tok < Lc) {
                 const float2 gt = G(i)[tok];
                 const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(G(i)[C - 1], gt);
@@ -292,7 +303,8 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int b = 0; b < DVP / 64; ++b)
-                        *reinterpret_cast<uint4 *>(sm + L::V + b * TILE + sw128_offset(tok, 8 * (4 * (tid >> 7) + q))) = z;
+                        *reinterpret_cast<uint4 *>(sm + L::V + (NS == 1 ? 0u : (i & 1) * L::VT) + b * TILE +
+                                                    sw128_offset(tok, 8 * (4 * (tid >> 7) + q))) = z;
             }
             done(D_SCALE);
             if (kMode != kOut) continue;
@@ -329,6 +341,7 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
         }
     } else if (warp < 16) {
         // ------------------------------------------------- state, outputs
+        regs_inc<120>();
         const int quarter = warp & 3, half = (warp >> 2) & 1, r = 32 * quarter + lane, col = NX * half;
         const uint32_t tlane = (uint32_t)(32 * quarter) << 16;
         const size_t row_off = (size_t)r * p.dk + col;
@@ -371,8 +384,24 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
                 }
                 __syncwarp();
             }
-            wait(C_X, i);
-            if (!ok) break;
+            const int oc = NO * half;
+            if (kMode == kOut) {
+                if (!wait(C_QS, i)) break;
+                tc_fence_after();
+                const float since = p.scale * hla_decay(G(i)[r], g0);
+#pragma unroll
+                for (int q = 0; q < NO / 16; ++q) {
+                    float v[16];
+                    tmem_ld16(tmem + tlane + TO + oc + 16u * q, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] *= since;
+                    tmem_st16(tmem + tlane + TO + oc + 16u * q, v);
+                }
+                tmem_wait_st();
+                done(D_O);
+            }
+            if (!wait(C_X, i)) break;
             tc_fence_after();
             const float keep = hla_decay(G(i)[C - 1], g0);
             total *= keep;
@@ -386,40 +415,45 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
             }
             done(D_X);
             if (kMode != kOut) continue;
-            wait(C_QS, i);
-            if (!ok) break;
-            tc_fence_after();
-            const float since = p.scale * hla_decay(G(i)[r], g0);
-            const int oc = NO * half;
-#pragma unroll
-            for (int q = 0; q < NO / 16; ++q) {
-                float v[16];
-                tmem_ld16(tmem + tlane + TO + oc + 16u * q, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= since;
-                tmem_st16(tmem + tlane + TO + oc + 16u * q, v);
-            }
-            tmem_wait_st();
-            done(D_O);
             if (i + 1 < nc) {
                 operand();
                 done(D_S);
             }
-            wait(C_PV, i);
-            if (!ok) break;
+            if (!wait(C_PV, i)) break;
             tc_fence_after();
+            // a full chunk leaves through a staging tile of the warp's 32 rows and 32 columns at a time (64-byte
+            // swizzled rows) by tensor stores; a partial one directly: one 16-byte piece per row and instruction, which
+            // costs the LSU four times the full tile's
             const int Lc = rows_of(i);
-            uint8_t *out = static_cast<uint8_t *>(p.o) + (((size_t)(row_of(i) + r) * p.H + h) * p.dv + oc) * 2;
+            uint8_t *stage = sm + L::O + (warp - 8) * 2 * KB;
 #pragma unroll
-            for (int q = 0; q < NO / 16; ++q) {
-                float v[16];
-                tmem_ld16(tmem + tlane + TO + oc + 16u * q, v);
+            for (int k = 0; k < NO / 32; ++k) {
+                const int c = oc + 32 * k;
+                float v[32];
+                tmem_ld16(tmem + tlane + TO + c, *reinterpret_cast<float(*)[16]>(v));
+                tmem_ld16(tmem + tlane + TO + c + 16u, *reinterpret_cast<float(*)[16]>(v + 16));
                 tmem_wait_ld();
-                if (r < Lc && oc + 16 * q < p.dv) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(out + 32 * q);
-                    dst[0] = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
-                    dst[1] = make_uint4(pack_bf2(v[8], v[9]), pack_bf2(v[10], v[11]), pack_bf2(v[12], v[13]), pack_bf2(v[14], v[15]));
+                uint4 w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = make_uint4(pack_bf2(v[8 * e], v[8 * e + 1]), pack_bf2(v[8 * e + 2], v[8 * e + 3]),
+                                      pack_bf2(v[8 * e + 4], v[8 * e + 5]), pack_bf2(v[8 * e + 6], v[8 * e + 7]));
+                if (Lc == C) {
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(stage + 64 * lane + 16 * (e ^ ((lane >> 1) & 3))) = w[e];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && c < p.dv) {
+                        tma_store_3d(&tm_o, stage, c, h, (int)(row_of(i) + 32 * quarter));
+                        bulk_commit();
+                    }
+                    __syncwarp();
+                } else if (r < Lc && c < p.dv) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + ((size_t)(row_of(i) + r) * p.H + h) * p.dv + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[e] = w[e];
                 }
             }
             done(D_E);
@@ -430,14 +464,12 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
                 if (col + e < p.dk) *reinterpret_cast<float4 *>(end + row_off + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         }
         if (kMode == kEnds && ok && tid == 256) s.seg_keep[dir][su * p.H + h] = total;
-        if (kMode == kStates && tid == 256) bulk_wait_read_all();
-    } else if (warp == 16) {
-        // ----------------------------------------------------- products
-        if (lane == 0) {
+        if (kMode != kEnds && lane == 0) bulk_wait_read_all();
+    } else {
+        regs_dec<64>();
+        if (warp == 16 && lane == 0) {
+            // ------------------------------------------------- products
             const Opnd oQ{sbase + L::Q, false, TILE, 0}, oK{sbase + L::K, false, TILE, 0}, oS{sbase + L::S, false, DVP * 128, 0};
-            // (a 64-row dv is read twice as the upper half of M: lanes that nothing reads)
-            const Opnd oVt{sbase + L::V, true, 0, DVP == 128 ? TILE : 0u}, oHi{sbase + L::HI, true, 0, TILE}, oLo{sbase + L::LO, true, 0, TILE};
-            const uint64_t dV = smem_desc_sw128(sbase + L::V, TILE, 1024u);
             constexpr uint32_t idX = idesc_bf16_f32(128, DKP, 1, 1), idS = idesc_bf16_f32(128, 128, 0, 0), idO = idesc_bf16_f32(128, DVP, 0, 0),
                                idP = idesc_bf16_f32(128, DVP, 0, 1);
             for (int i = 0; i < nc && ok; ++i) {
@@ -445,28 +477,31 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
                     wait(F_K, i);
                     if (!wait(F_Q, i)) break;
                     tc_fence_after();
-                    mma_chain<DKP / 16>(tmem + TS, oQ, oK, idS, false);  // (the scores before were read before D_P, waited for below)
+                    mma_chain<DKP / 16>(tmem + TS, oQ, oK, idS, false);  // (D_P of the chunk before: its scores are read)
                     mma_commit(bars + C_QK);
-                }
-                wait(D_SCALE, i);
-                wait(F_V, i);
-                if (i > 0) wait(D_X, i - 1);
-                if (!ok) break;
-                tc_fence_after();
-                mma_chain<C / 16>(tmem + TX, oVt, oHi, idX, false);
-                mma_chain<C / 16>(tmem + TX, oVt, oLo, idX, true);
-                mma_commit(bars + C_X);
-                if (kMode == kOut) {
                     wait(D_S, i);
                     if (i > 0) wait(D_E, i - 1);
                     if (!ok) break;
                     tc_fence_after();
                     mma_chain<DKP / 16>(tmem + TO, oQ, oS, idO, false);
                     mma_commit(bars + C_QS);
+                }
+                wait(D_SCALE, i);
+                wait_tile(F_V, i);
+                if (i > 0) wait(D_X, i - 1);
+                if (!ok) break;
+                tc_fence_after();
+                // (a 64-row dv is read twice as the upper half of M: lanes that nothing reads)
+                const uint32_t st = NS == 1 ? 0u : (uint32_t)(i & 1), vb = sbase + L::V + st * L::VT;
+                const Opnd oVt{vb, true, 0, DVP == 128 ? TILE : 0u};
+                mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::HI + st * L::KT, true, 0, TILE}, idX, false);
+                mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::LO, true, 0, TILE}, idX, true);
+                mma_commit(bars + C_X);
+                if (kMode == kOut) {
                     wait(D_P, i);
-                    wait(D_O, i);
-                    if (!ok) break;
+                    if (!wait(D_O, i)) break;
                     tc_fence_after();
+                    const uint64_t dV = smem_desc_sw128(vb, TILE, 1024u);
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k) mma_bf16_ts(tmem + TO, tmem + TP + 8u * k, dV + (uint64_t)((k * 2048u) >> 4), idP, 1u);
                     mma_commit(bars + C_PV);
@@ -474,51 +509,64 @@ __global__ void __launch_bounds__(576, 1) hla_chain_tc_kernel(const __grid_const
             }
             mma_commit(bars + C_END);  // nothing may be in flight when TMEM is freed
             ok = mbar_wait_bounded(bars + C_END, 0, kWaitCycles) && ok;
-        }
-        __syncwarp();
-    } else if (lane == 0) {
-        // ------------------------------------------------------- copies
-        const CUtensorMap *ta = dir ? &tm_q : &tm_k, *tb = dir ? &tm_o : &tm_v;
-        int issued_k = 0, issued_q = 0, issued_v = 0;
-        for (int i = 0; i < nc && ok; ++i) {
-            const int tok = (int)row_of(i), next = i + 1 < nc ? (int)row_of(i + 1) : -1;
-            if (i > 0) {
-                wait(D_SCALE, i - 1);
-                if (kMode == kOut) wait(C_QK, i - 1);
-            }
-            // (the gates' ring: chunk i - 4's outputs are stored once chunk i - 1's scores are done, or its increment)
-            if (!ok) break;
-            mbar_arrive_expect_tx(bars + F_K, L::KB_ + GATE);
-            ++issued_k;
-            bulk_load(sm + L::G + (i & 3) * GATE, s.gates + ((size_t)(sp.slot + chunk(i)) * p.H + h) * GATE, GATE, bars + F_K);
-#pragma unroll
-            for (int b = 0; b < DKP / 64; ++b) {
-                tma_load_3d(sm + L::K + b * TILE, ta, bars + F_K, 64 * b, h, tok);
-                if (next >= 0) tma_prefetch_l2_3d(ta, 64 * b, h, next);
-            }
-            if (kMode == kOut) {
-                if (i > 0 && !wait(C_QS, i - 1)) break;
-                mbar_arrive_expect_tx(bars + F_Q, L::KB_);
-                ++issued_q;
+        } else if (warp == 17 && lane == 0) {
+            // --------------------------------------------------- copies
+            const CUtensorMap *ta = dir ? &tm_q : &tm_k, *tb = dir ? &tm_o : &tm_v;
+            int nk = 0, nq = 0, nv = 0;  // loads issued
+            for (int i = 0; i < nc && ok; ++i) {
+                const int tok = (int)row_of(i), ahead = i + 2 < nc ? (int)row_of(i + 2) : -1;
+                const uint32_t st = NS == 1 ? 0u : (uint32_t)(i & 1);
+                if (kMode == kOut) {
+                    if (i > 0) {
+                        wait(D_SCALE, i - 1);
+                        wait(C_QK, i - 1);
+                    }
+                } else if (i > 1) {
+                    wait(C_X, i - 2);
+                    wait(D_X, i - 2);  // (the gates' ring)
+                }
+                // The gates' ring: what reads chunk i - 4's is done, before chunk i - 2's D_O that Q K^T of chunk i - 1
+                // was issued after, or before its D_X.
+                if (!ok) break;
+                mbar_arrive_expect_tx(bars + F_K + st, L::KT + GATE);
+                ++nk;
+                bulk_load(sm + L::G + (i & 3) * GATE, s.gates + ((size_t)(sp.slot + chunk(i)) * p.H + h) * GATE, GATE, bars + F_K + st);
 #pragma unroll
                 for (int b = 0; b < DKP / 64; ++b) {
-                    tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + F_Q, 64 * b, h, tok);
-                    if (next >= 0) tma_prefetch_l2_3d(&tm_q, 64 * b, h, next);
+                    tma_load_3d(sm + L::K + st * L::KT + b * TILE, ta, bars + F_K + st, 64 * b, h, tok);
+                    if (ahead >= 0) tma_prefetch_l2_3d(ta, 64 * b, h, ahead);
+                }
+                if (kMode == kOut) {
+                    if (i > 0 && !wait(C_QS, i - 1)) break;
+                    mbar_arrive_expect_tx(bars + F_Q, L::KT);
+                    ++nq;
+#pragma unroll
+                    for (int b = 0; b < DKP / 64; ++b) {
+                        tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + F_Q, 64 * b, h, tok);
+                        if (ahead >= 0) tma_prefetch_l2_3d(&tm_q, 64 * b, h, ahead);
+                    }
+                    if (i > 0 && !wait(C_PV, i - 1)) break;  // (and the products before it)
+                }
+                mbar_arrive_expect_tx(bars + F_V + st, L::VT);
+                ++nv;
+#pragma unroll
+                for (int b = 0; b < DVP / 64; ++b) {
+                    tma_load_3d(sm + L::V + st * L::VT + b * TILE, tb, bars + F_V + st, 64 * b, h, tok);
+                    if (ahead >= 0) tma_prefetch_l2_3d(tb, 64 * b, h, ahead);
                 }
             }
-            if (i > 0 && !wait(kMode == kOut ? C_PV : C_X, i - 1)) break;  // (products end in order)
-            mbar_arrive_expect_tx(bars + F_V, L::VB);
-            ++issued_v;
-#pragma unroll
-            for (int b = 0; b < DVP / 64; ++b) {
-                tma_load_3d(sm + L::V + b * TILE, tb, bars + F_V, 64 * b, h, tok);
-                if (next >= 0) tma_prefetch_l2_3d(tb, 64 * b, h, next);
-            }
+            // nothing may be in flight when the CTA ends: the last loads into each buffer (bounded)
+            const auto drain = [&](int b, int issued) {
+                for (int st = 0; st < NS; ++st) {
+                    const int of = NS == 1 ? issued : (issued + 1 - st) / 2;  // loads into this buffer
+                    if (of > 0) mbar_wait_bounded(bars + b + st, (uint32_t)(of - 1) & 1u, kWaitCycles);
+                }
+            };
+            drain(F_K, nk);
+            drain(F_V, nv);
+            if (nq > 0) mbar_wait_bounded(bars + F_Q, (uint32_t)(nq - 1) & 1u, kWaitCycles);
         }
-        // nothing may be in flight when the CTA ends: the last copies of each kind (bounded)
-        if (issued_k) mbar_wait_bounded(bars + F_K, (uint32_t)(issued_k - 1) & 1u, kWaitCycles);
-        if (issued_q) mbar_wait_bounded(bars + F_Q, (uint32_t)(issued_q - 1) & 1u, kWaitCycles);
-        if (issued_v) mbar_wait_bounded(bars + F_V, (uint32_t)(issued_v - 1) & 1u, kWaitCycles);
+        __syncwarp();
     }
     if (!ok && p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
     tc_fence_before();
@@ -943,15 +991,17 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
 
 // ================================================================== host
 // 3-D map over a token-major [tokens, H, d] bf16 tensor; box of 64 channels (zeros past d) and 128 tokens.
-bool make_tile_map(CUtensorMap *m, const void *base, size_t tokens, int H, int d) {
+// `rows` and `cols`: another box, of 32 rows and 32 channels in 64-byte swizzled rows (the outputs' staging).
+bool make_tile_map(CUtensorMap *m, const void *base, size_t tokens, int H, int d, int cols = 64, int rows = C) {
     auto enc = tc::get_encode();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
-    cuuint32_t box[3] = {64, 1, (cuuint32_t)C};
+    cuuint32_t box[3] = {(cuuint32_t)cols, 1, (cuuint32_t)rows};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1006,7 +1056,7 @@ cudaError_t chain(const ChainArgs &s, const Maps &m, const Layout &l, int dirs) 
     constexpr size_t bytes = ChainSmem<DKP, DVP, kMode>::bytes;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)((l.sc ? l.seg_slots : s.a.N) * s.a.H), 1, dirs), 576, bytes, s.a.stream>>>(m.k, m.v, m.q, m.o, s);
+    kern<<<dim3((unsigned)((l.sc ? l.seg_slots : s.a.N) * s.a.H), 1, dirs), kChainThreads, bytes, s.a.stream>>>(m.k, m.v, m.q, m.o, s);
     return cudaGetLastError();
 }
 
@@ -1015,7 +1065,8 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     const size_t tokens = (size_t)a.B * a.T;
     Maps m;
     if (!make_tile_map(&m.q, a.q, tokens, a.H, a.dk) || !make_tile_map(&m.k, a.k, tokens, a.H, a.dk) ||
-        !make_tile_map(&m.v, a.v, tokens, a.H, a.dv) || !make_tile_map(&m.o, back ? a.dO : a.v, tokens, a.H, a.dv))
+        !make_tile_map(&m.v, a.v, tokens, a.H, a.dv) ||
+        !(back ? make_tile_map(&m.o, a.dO, tokens, a.H, a.dv) : make_tile_map(&m.o, a.o, tokens, a.H, a.dv, 32, 32)))
         return cudaErrorInvalidValue;
     if (back && (!make_tile_map(&m.dq, a.dq, tokens, a.H, a.dk) || !make_tile_map(&m.dk, a.dk_, tokens, a.H, a.dk) ||
                  !make_tile_map(&m.dv, a.dv_, tokens, a.H, a.dv)))
