@@ -614,10 +614,11 @@ struct TileArgs {
     HlaArgs a;
     const uint8_t *gates;
     const uint8_t *S, *R;   // the chunks' incoming states, and the gradients of their outgoing ones
-    unsigned ahead;         // CTAs that run at once: the tile this many further on is prefetched into L2
+    unsigned tiles;         // chunk slots x heads
 };
 
-// All gradients of a (chunk, head), by one CTA of 512 threads. With P = Q K^T and dP = dO V^T (both [row r, column
+// All gradients of a (chunk, head), by 512 threads; one CTA per SM, which goes through its tiles with the next one's
+// copies under way: q and k as soon as their products are done, the rest as the places fall free. With P = Q K^T and dP = dO V^T (both [row r, column
 // s], so that one decay D_rs serves both), A = scale P . D and dA = scale dP . D in bf16:
 //   dQ = dA K   + scale e^{G_r} dO S      accumulators T2
 //   dK = dA^T Q + e^{G_C - G_r} V R       T3
@@ -630,9 +631,12 @@ struct GradTile {
     static constexpr bool over = DKP == 128 && DVP == 128;
     static constexpr uint32_t Q = 0, K = QB, V = 2 * QB, O = V + VB, S = O + VB, R = S + SB;
     static constexpr uint32_t A = over ? S : R + SB, dA = over ? V : A + 2 * TILE, END = over ? R + SB : dA + 2 * TILE;
-    static constexpr uint32_t G = END + 128, RED = G + GATE;   // RED: 3 x 4 x 128 floats, and 16
+    // the results' staging: where nothing is read any more by then, and not over q and k, whose next tiles come first
+    static constexpr uint32_t stQ = over ? R : S, stK = dA, stV = A;
+    static constexpr uint32_t G = END + 128, RED = G + 2 * GATE;   // RED: 3 x 4 x 128 floats, and 16
     static constexpr uint32_t bytes = RED + 12 * C * 4 + 64 + 1024;
     static_assert(bytes <= 232448, "shared memory budget");
+    static_assert(over || QB <= 2 * SB, "dQ is staged over S and R");
 };
 
 template <int DKP, int DVP>
@@ -642,67 +646,46 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
                                                              const __grid_constant__ CUtensorMap tm_dv, const TileArgs t) {
     using L = GradTile<DKP, DVP>;
     const HlaArgs &p = t.a;
-    const long long slot = blockIdx.x / p.H;
-    const int h = blockIdx.x % p.H;
-    int n, c;
-    HlaSpan sp;
-    if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
+    struct Tile {
+        unsigned i;
+        long long slot, row0;
+        int h, Lc;
+        bool hasS, hasR;
+    };
+    // the first tile at or after i of this CTA's that has a chunk
+    const auto find = [&](unsigned i, Tile &x) {
+        for (; i < t.tiles; i += gridDim.x) {
+            int n, c;
+            HlaSpan sp;
+            x.slot = i / p.H;
+            if (!hla_chunk_of(p, x.slot, C, n, c, sp)) continue;
+            x.i = i;
+            x.h = i % p.H;
+            x.row0 = sp.t0 + (long long)c * C;
+            x.Lc = min(C, sp.len - c * C);
+            x.hasS = p.S0 != nullptr || c > 0;
+            x.hasR = p.dST != nullptr || c + 1 < sp.nch;
+            return true;
+        }
+        return false;
+    };
+    Tile cur;
+    if (!find(blockIdx.x, cur)) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
-    // loads: q k, v dO, S R; products: P, dP, dO S and V R, K R^T, dA K and dA^T Q, A^T dO
+    // loads: q k, v dO, S R; products: P, dP, dO S and V R, K R^T, dA K and dA^T Q, A^T dO. One phase per tile.
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::END);
-    enum { L_QK, L_VO, L_SR, B_P, B_DP, B_SR, B_KR, B_QK, B_V, NBAR };
+    enum { L_QK, L_VO, L_SR, B_P, B_DP, B_SR, B_KR, B_QK, B_V, B_END, NBAR };
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + NBAR);
-    const float2 *G = reinterpret_cast<const float2 *>(sm + L::G);
     float *red = reinterpret_cast<float *>(sm + L::RED);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, grp = warp >> 2;
-    const long long row0 = sp.t0 + (long long)c * C;
-    const int Lc = min(C, sp.len - c * C);
-    const bool hasS = p.S0 != nullptr || c > 0, hasR = p.dST != nullptr || c + 1 < sp.nch;
-
+    const bool issuer = tid == 0, copier = tid == 96;  // the threads that issue the products, and the copies
     if (tid == 0) {
         for (int i = 0; i < NBAR; ++i) mbar_init(bars + i, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(bars + L_QK, 2 * L::QB + GATE);
-        bulk_load(sm + L::G, t.gates + ((size_t)slot * p.H + h) * GATE, GATE, bars + L_QK);
-#pragma unroll
-        for (int b = 0; b < DKP / 64; ++b) {
-            tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + L_QK, 64 * b, h, (int)row0);
-            tma_load_3d(sm + L::K + b * TILE, &tm_k, bars + L_QK, 64 * b, h, (int)row0);
-        }
-        mbar_arrive_expect_tx(bars + L_VO, 2 * L::VB);
-#pragma unroll
-        for (int b = 0; b < DVP / 64; ++b) {
-            tma_load_3d(sm + L::V + b * TILE, &tm_v, bars + L_VO, 64 * b, h, (int)row0);
-            tma_load_3d(sm + L::O + b * TILE, &tm_o, bars + L_VO, 64 * b, h, (int)row0);
-        }
-        mbar_arrive_expect_tx(bars + L_SR, (hasS ? L::SB : 0u) + (hasR ? L::SB : 0u));
-        const size_t at = ((size_t)slot * p.H + h) * blob_bytes(DKP, DVP);
-        if (hasS) bulk_load(sm + L::S, t.S + at, L::SB, bars + L_SR);
-        if (hasR) bulk_load(sm + L::R, t.R + at, L::SB, bars + L_SR);
-        // the tile that comes to this SM next (one CTA per SM) starts on its way from HBM now
-        const unsigned nb = blockIdx.x + t.ahead;
-        int n2, c2;
-        HlaSpan s2;
-        if (nb < gridDim.x && hla_chunk_of(p, nb / p.H, C, n2, c2, s2)) {
-            const int h2 = nb % p.H, row2 = (int)(s2.t0 + (long long)c2 * C);
-            const size_t at2 = ((size_t)(nb / p.H) * p.H + h2) * blob_bytes(DKP, DVP);
-#pragma unroll
-            for (int b = 0; b < DKP / 64; ++b) {
-                tma_prefetch_l2_3d(&tm_q, 64 * b, h2, row2);
-                tma_prefetch_l2_3d(&tm_k, 64 * b, h2, row2);
-            }
-#pragma unroll
-            for (int b = 0; b < DVP / 64; ++b) {
-                tma_prefetch_l2_3d(&tm_v, 64 * b, h2, row2);
-                tma_prefetch_l2_3d(&tm_o, 64 * b, h2, row2);
-            }
-            bulk_prefetch_l2(t.S + at2, L::SB);
-            bulk_prefetch_l2(t.R + at2, L::SB);
-        }
     }
     if (warp == 0) {
         __syncwarp();
@@ -716,134 +699,196 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
     constexpr uint32_t T0 = 0, T1 = 128, T2 = 256, T3 = 384;
     const int r = 32 * quarter + lane, col = 32 * grp;   // this thread's row, and its 32 columns
     const float2 g0 = make_float2(0.f, 0.f);
-    const auto zero16 = [&](uint32_t off) { *reinterpret_cast<uint4 *>(sm + off) = make_uint4(0, 0, 0, 0); };
 
-    bool ok = true;
-    const auto wait = [&](int b) { ok = mbar_wait_bounded(bars + b, 0, kWaitCycles) && ok; };
-    if (Lc < C) {  // rows behind the sequence's end: zero in every operand, whatever stands there
-        wait(L_QK);
-        wait(L_VO);
-        for (int i = tid; i < (C - Lc) * 8; i += 512) {
-            const uint32_t off = sw128_offset(Lc + (i >> 3), 8 * (i & 7));
+    // the copier's loads of tile x, the it-th of this CTA
+    int loads[3] = {0, 0, 0};
+    const auto load_qk = [&](const Tile &x, int it) {
+        mbar_arrive_expect_tx(bars + L_QK, 2 * L::QB + GATE);
+        ++loads[0];
+        bulk_load(sm + L::G + (it & 1) * GATE, t.gates + ((size_t)x.slot * p.H + x.h) * GATE, GATE, bars + L_QK);
 #pragma unroll
-            for (int b = 0; b < DKP / 64; ++b) {
-                zero16(L::Q + b * TILE + off);
-                zero16(L::K + b * TILE + off);
+        for (int b = 0; b < DKP / 64; ++b) {
+            tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + L_QK, 64 * b, x.h, (int)x.row0);
+            tma_load_3d(sm + L::K + b * TILE, &tm_k, bars + L_QK, 64 * b, x.h, (int)x.row0);
+        }
+    };
+    const auto load_o = [&](const Tile &x) {
+        mbar_arrive_expect_tx(bars + L_VO, 2 * L::VB);
+        ++loads[1];
+#pragma unroll
+        for (int b = 0; b < DVP / 64; ++b) tma_load_3d(sm + L::O + b * TILE, &tm_o, bars + L_VO, 64 * b, x.h, (int)x.row0);
+    };
+    const auto load_vsr = [&](const Tile &x) {
+#pragma unroll
+        for (int b = 0; b < DVP / 64; ++b) tma_load_3d(sm + L::V + b * TILE, &tm_v, bars + L_VO, 64 * b, x.h, (int)x.row0);
+        mbar_arrive_expect_tx(bars + L_SR, (x.hasS ? L::SB : 0u) + (x.hasR ? L::SB : 0u));
+        ++loads[2];
+        const size_t at = ((size_t)x.slot * p.H + x.h) * blob_bytes(DKP, DVP);
+        if (x.hasS) bulk_load(sm + L::S, t.S + at, L::SB, bars + L_SR);
+        if (x.hasR) bulk_load(sm + L::R, t.R + at, L::SB, bars + L_SR);
+    };
+    const auto prefetch = [&](const Tile &x) {
+        const size_t at = ((size_t)x.slot * p.H + x.h) * blob_bytes(DKP, DVP);
+#pragma unroll
+        for (int b = 0; b < DKP / 64; ++b) {
+            tma_prefetch_l2_3d(&tm_q, 64 * b, x.h, (int)x.row0);
+            tma_prefetch_l2_3d(&tm_k, 64 * b, x.h, (int)x.row0);
+        }
+#pragma unroll
+        for (int b = 0; b < DVP / 64; ++b) {
+            tma_prefetch_l2_3d(&tm_v, 64 * b, x.h, (int)x.row0);
+            tma_prefetch_l2_3d(&tm_o, 64 * b, x.h, (int)x.row0);
+        }
+        if (x.hasS) bulk_prefetch_l2(t.S + at, L::SB);
+        if (x.hasR) bulk_prefetch_l2(t.R + at, L::SB);
+    };
+    if (copier) {
+        load_qk(cur, 0);
+        load_o(cur);
+        load_vsr(cur);
+    }
+    __syncwarp();
+
+    const Opnd oQ{sbase + L::Q, false, TILE, 0}, oK{sbase + L::K, false, TILE, 0}, oV{sbase + L::V, false, TILE, 0}, oO{sbase + L::O, false, TILE, 0};
+    const auto zero16 = [&](uint32_t off) { *reinterpret_cast<uint4 *>(sm + off) = make_uint4(0, 0, 0, 0); };
+    bool bad = false;
+    for (int it = 0;; ++it) {
+        Tile nxt;
+        const bool more = find(cur.i + gridDim.x, nxt);
+        const uint32_t ph = it & 1;
+        const int Lc = cur.Lc;
+        const bool hasS = cur.hasS, hasR = cur.hasR;
+        const float2 *G = reinterpret_cast<const float2 *>(sm + L::G + ph * GATE);
+        bool ok = true;
+        const auto wait = [&](int b) { ok = ok && mbar_wait_bounded(bars + b, ph, kWaitCycles); };
+        if (Lc < C) {  // rows behind the sequence's end: zero in every operand, whatever stands there
+            wait(L_QK);
+            wait(L_VO);
+            for (int i = tid; i < (C - Lc) * 8; i += 512) {
+                const uint32_t off = sw128_offset(Lc + (i >> 3), 8 * (i & 7));
+#pragma unroll
+                for (int b = 0; b < DKP / 64; ++b) {
+                    zero16(L::Q + b * TILE + off);
+                    zero16(L::K + b * TILE + off);
+                }
+#pragma unroll
+                for (int b = 0; b < DVP / 64; ++b) {
+                    zero16(L::V + b * TILE + off);
+                    zero16(L::O + b * TILE + off);
+                }
             }
+            fence_proxy_async_smem();
+            __syncthreads();
+        }
+        if (issuer) {
+            wait(L_QK);
+            if (ok) {
+                tc_fence_after();
+                mma_chain<DKP / 16>(tmem + T0, oQ, oK, idesc_bf16_f32(128, 128, 0, 0), false);
+                mma_commit(bars + B_P);
+            }
+            wait(L_VO);
+            if (ok) {
+                mma_chain<DVP / 16>(tmem + T1, oO, oV, idesc_bf16_f32(128, 128, 0, 0), false);
+                mma_commit(bars + B_DP);
+            }
+            wait(L_SR);
+            if (ok) {  // S, R as [dv rows][dk]: dk is the result's column
+                if (hasS) mma_chain<DVP / 16>(tmem + T2, oO, Opnd{sbase + L::S, true, 0, DVP * 128}, idesc_bf16_f32(128, DKP, 0, 1), false);
+                if (hasR) mma_chain<DVP / 16>(tmem + T3, oV, Opnd{sbase + L::R, true, 0, DVP * 128}, idesc_bf16_f32(128, DKP, 0, 1), false);
+                mma_commit(bars + B_SR);
+            }
+        }
+        __syncwarp();
+        if (copier && more) prefetch(nxt);  // the next tile on its way into L2
+        __syncwarp();
+        float thr = 0.f;
+        if (p.dg && hasS && hasR) {  // <S, R>
+            wait(L_SR);
+            if (ok) {
 #pragma unroll
-            for (int b = 0; b < DVP / 64; ++b) {
-                zero16(L::V + b * TILE + off);
-                zero16(L::O + b * TILE + off);
+                for (int i = 0; i < (int)(L::SB / 16 / 512); ++i) {
+                    const uint32_t off = 16u * (tid + 512 * i);
+                    const uint4 a = *reinterpret_cast<const uint4 *>(sm + L::S + off), b = *reinterpret_cast<const uint4 *>(sm + L::R + off);
+                    thr = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), thr));
+                    thr = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), thr));
+                    thr = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), thr));
+                    thr = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), thr));
+                }
+            }
+        }
+        // A and dA of this thread's row and columns, in bf16 pairs
+        uint32_t wa[16], wd[16];
+        wait(L_QK);  // (the gates came with q and k)
+        wait(B_P);
+        wait(B_DP);
+        tc_fence_after();
+        const float2 gr = G[r];
+        const DecayRow dr{G, reinterpret_cast<const float *>(G + C), gr, r, 32 * quarter, Lc, p.scale};
+        if (dr.none(col)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) wa[e] = wd[e] = 0u;
+        } else if (ok) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float a[16], d[16], f[16];
+                tmem_ld16(tmem + tlane + T0 + col + 16u * q, a);
+                tmem_ld16(tmem + tlane + T1 + col + 16u * q, d);
+                dr.get(col, q, f);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = col + 16 * q + 2 * e;
+                    wa[8 * q + e] = pack_bf2(dr.keep(c, a[2 * e], f[2 * e]), dr.keep(c + 1, a[2 * e + 1], f[2 * e + 1]));
+                    wd[8 * q + e] = pack_bf2(dr.keep(c, d[2 * e], f[2 * e]), dr.keep(c + 1, d[2 * e + 1], f[2 * e + 1]));
+                }
+            }
+        }
+        wait(B_SR);  // the products have read S and V ..
+        __syncthreads();  // .. and every thread its part of S
+        if (ok) {
+            uint8_t *da = sm + L::A + (col >> 6) * TILE, *dd = sm + L::dA + (col >> 6) * TILE;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t off = sw128_offset(r, (col & 63) + 8 * q);
+                *reinterpret_cast<uint4 *>(da + off) = make_uint4(wa[4 * q], wa[4 * q + 1], wa[4 * q + 2], wa[4 * q + 3]);
+                *reinterpret_cast<uint4 *>(dd + off) = make_uint4(wd[4 * q], wd[4 * q + 1], wd[4 * q + 2], wd[4 * q + 3]);
             }
         }
         fence_proxy_async_smem();
-        __syncthreads();
-    }
-    const Opnd oQ{sbase + L::Q, false, TILE, 0}, oK{sbase + L::K, false, TILE, 0}, oV{sbase + L::V, false, TILE, 0}, oO{sbase + L::O, false, TILE, 0};
-    if (tid == 0) {
-        wait(L_QK);
-        if (ok) {
-            mma_chain<DKP / 16>(tmem + T0, oQ, oK, idesc_bf16_f32(128, 128, 0, 0), false);
-            mma_commit(bars + B_P);
-        }
-        wait(L_VO);
-        if (ok) {
-            mma_chain<DVP / 16>(tmem + T1, oO, oV, idesc_bf16_f32(128, 128, 0, 0), false);
-            mma_commit(bars + B_DP);
-        }
-        wait(L_SR);
-        if (ok) {  // S, R as [dv rows][dk]: dk is the result's column
-            if (hasS) mma_chain<DVP / 16>(tmem + T2, oO, Opnd{sbase + L::S, true, 0, DVP * 128}, idesc_bf16_f32(128, DKP, 0, 1), false);
-            if (hasR) mma_chain<DVP / 16>(tmem + T3, oV, Opnd{sbase + L::R, true, 0, DVP * 128}, idesc_bf16_f32(128, DKP, 0, 1), false);
-            mma_commit(bars + B_SR);
-        }
-    }
-    __syncwarp();
-    float thr = 0.f;
-    if (p.dg && hasS && hasR) {  // <S, R>
-        wait(L_SR);
-        if (ok) {
+        tc_fence_before();
+        // the state's products scaled per row in TMEM; sums of k . dK2 on the way
+        const float since = p.scale * hla_decay(gr, g0), until = hla_decay(G[C - 1], gr);
+        float cs2 = 0.f, cs = 0.f, rs = 0.f;
+        const auto dot16 = [&](uint32_t tile, int cl, const float *v) {
+            float x = 0.f;
 #pragma unroll
-            for (int i = 0; i < (int)(L::SB / 16 / 512); ++i) {
-                const uint32_t off = 16u * (tid + 512 * i);
-                const uint4 a = *reinterpret_cast<const uint4 *>(sm + L::S + off), b = *reinterpret_cast<const uint4 *>(sm + L::R + off);
-                thr = fmaf(bf_lo(a.x), bf_lo(b.x), fmaf(bf_hi(a.x), bf_hi(b.x), thr));
-                thr = fmaf(bf_lo(a.y), bf_lo(b.y), fmaf(bf_hi(a.y), bf_hi(b.y), thr));
-                thr = fmaf(bf_lo(a.z), bf_lo(b.z), fmaf(bf_hi(a.z), bf_hi(b.z), thr));
-                thr = fmaf(bf_lo(a.w), bf_lo(b.w), fmaf(bf_hi(a.w), bf_hi(b.w), thr));
+            for (int q = 0; q < 2; ++q) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(sm + tile + (cl >> 6) * TILE + sw128_offset(r, (cl & 63) + 8 * q));
+                const uint32_t in[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x = fmaf(bf_lo(in[e]), v[8 * q + 2 * e], fmaf(bf_hi(in[e]), v[8 * q + 2 * e + 1], x));
             }
-        }
-    }
-    // A and dA of this thread's row and columns, in bf16 pairs
-    uint32_t wa[16], wd[16];
-    wait(B_P);
-    wait(B_DP);
-    tc_fence_after();
-    wait(L_QK);  // (the gates came with q and k)
-    const float2 gr = G[r];
-    const DecayRow dr{G, reinterpret_cast<const float *>(G + C), gr, r, 32 * quarter, Lc, p.scale};
-    if (dr.none(col)) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) wa[e] = wd[e] = 0u;
-    } else if (ok) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float a[16], d[16], f[16];
-            tmem_ld16(tmem + tlane + T0 + col + 16u * q, a);
-            tmem_ld16(tmem + tlane + T1 + col + 16u * q, d);
-            dr.get(col, q, f);
+            return x;
+        };
+        const auto load32 = [&](uint32_t T, float (&v)[32]) {
+            tmem_ld16(tmem + tlane + T + col, *reinterpret_cast<float(*)[16]>(v));
+            tmem_ld16(tmem + tlane + T + col + 16u, *reinterpret_cast<float(*)[16]>(v + 16));
             tmem_wait_ld();
+        };
+        const auto scale_rows = [&](uint32_t T, float f) {
+            float v[32];
+            load32(T, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = col + 16 * q + 2 * e;
-                wa[8 * q + e] = pack_bf2(dr.keep(c, a[2 * e], f[2 * e]), dr.keep(c + 1, a[2 * e + 1], f[2 * e + 1]));
-                wd[8 * q + e] = pack_bf2(dr.keep(c, d[2 * e], f[2 * e]), dr.keep(c + 1, d[2 * e + 1], f[2 * e + 1]));
-            }
-        }
-    }
-    wait(B_SR);  // the products have read S and V ..
-    __syncthreads();  // .. and every thread its part of S
-    if (ok) {
-        uint8_t *da = sm + L::A + (col >> 6) * TILE, *dd = sm + L::dA + (col >> 6) * TILE;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t off = sw128_offset(r, (col & 63) + 8 * q);
-            *reinterpret_cast<uint4 *>(da + off) = make_uint4(wa[4 * q], wa[4 * q + 1], wa[4 * q + 2], wa[4 * q + 3]);
-            *reinterpret_cast<uint4 *>(dd + off) = make_uint4(wd[4 * q], wd[4 * q + 1], wd[4 * q + 2], wd[4 * q + 3]);
-        }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    // the state's products scaled per row in TMEM; sums of k . dK2 on the way
-    const float since = p.scale * hla_decay(gr, g0), until = hla_decay(G[C - 1], gr);
-    float cs2 = 0.f, cs = 0.f, rs = 0.f;
-    const auto dot16 = [&](uint32_t tile, int cl, const float (&v)[16]) {
-        float x = 0.f;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(sm + tile + (cl >> 6) * TILE + sw128_offset(r, (cl & 63) + 8 * q));
-            const uint32_t in[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x = fmaf(bf_lo(in[e]), v[8 * q + 2 * e], fmaf(bf_hi(in[e]), v[8 * q + 2 * e + 1], x));
-        }
-        return x;
-    };
-    const auto scale_rows = [&](uint32_t T, float f) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float v[16];
-            tmem_ld16(tmem + tlane + T + col + 16u * q, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= f;
-            tmem_st16(tmem + tlane + T + col + 16u * q, v);
-            if (T == T3 && p.dg) cs2 += dot16(L::K, col + 16 * q, v);
-        }
-        tmem_wait_st();
-    };
-    bool bad = __syncthreads_or(!ok);
-    if (!bad) {
-        if (tid == 0) {
+            for (int e = 0; e < 32; ++e) v[e] *= f;
+            tmem_st16(tmem + tlane + T + col, *reinterpret_cast<float(*)[16]>(v));
+            tmem_st16(tmem + tlane + T + col + 16u, *reinterpret_cast<float(*)[16]>(v + 16));
+            if (T == T3 && p.dg) cs2 = dot16(L::K, col, v) + dot16(L::K, col + 16, v + 16);
+            tmem_wait_st();
+        };
+        bad = __syncthreads_or(!ok);
+        if (bad) break;
+        if (issuer) {
             tc_fence_after();
             if (hasR) mma_chain<DKP / 16>(tmem + T1, oK, Opnd{sbase + L::R, false, DVP * 128, 0}, idesc_bf16_f32(128, DVP, 0, 0), false);
             mma_commit(bars + B_KR);
@@ -854,11 +899,10 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         if (hasR && col < DKP) scale_rows(T3, until);
         tc_fence_before();
         __syncthreads();
-        const Opnd aT{sbase + L::A, true, 0, TILE}, dT{sbase + L::dA, true, 0, TILE}, dN{sbase + L::dA, false, TILE, 0};
-        if (tid == 0) {
+        if (issuer) {
             tc_fence_after();
-            mma_chain<C / 16>(tmem + T2, dN, Opnd{sbase + L::K, true, 0, TILE}, idesc_bf16_f32(128, DKP, 0, 1), hasS);
-            mma_chain<C / 16>(tmem + T3, dT, Opnd{sbase + L::Q, true, 0, TILE}, idesc_bf16_f32(128, DKP, 1, 1), hasR);
+            mma_chain<C / 16>(tmem + T2, Opnd{sbase + L::dA, false, TILE, 0}, Opnd{sbase + L::K, true, 0, TILE}, idesc_bf16_f32(128, DKP, 0, 1), hasS);
+            mma_chain<C / 16>(tmem + T3, Opnd{sbase + L::dA, true, 0, TILE}, Opnd{sbase + L::Q, true, 0, TILE}, idesc_bf16_f32(128, DKP, 1, 1), hasR);
             mma_commit(bars + B_QK);
         }
         __syncwarp();
@@ -867,43 +911,34 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         if (ok && hasR && col < DVP) scale_rows(T1, until);
         tc_fence_before();
         bad = __syncthreads_or(!ok);
-        if (!bad) {
-            if (tid == 0) {
-                tc_fence_after();
-                mma_chain<C / 16>(tmem + T1, aT, Opnd{sbase + L::O, true, 0, TILE}, idesc_bf16_f32(128, DVP, 1, 1), hasR);
-                mma_commit(bars + B_V);
-            }
-            __syncwarp();
+        if (bad) break;
+        if (issuer) {
+            tc_fence_after();
+            mma_chain<C / 16>(tmem + T1, Opnd{sbase + L::A, true, 0, TILE}, Opnd{sbase + L::O, true, 0, TILE}, idesc_bf16_f32(128, DVP, 1, 1), hasR);
+            mma_commit(bars + B_V);
         }
-    }
-    // results: staged over q, k and (dA, or v), written by tensor stores; rows of a partial chunk directly
-    const auto result = [&](uint32_t T, uint32_t stage, void *out, int d, float *sum) {
+        __syncwarp();
+        // results: staged and written by tensor stores; rows of a partial chunk directly
+        const auto result = [&](uint32_t T, uint32_t stage, void *out, int d, uint32_t dots, float *sum) {
+            float v[32];
+            load32(T, v);
+            if (sum && p.dg) *sum = dot16(dots, col, v) + dot16(dots, col + 16, v + 16);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float v[16];
-            const int cl = col + 16 * q;
-            tmem_ld16(tmem + tlane + T + cl, v);
-            tmem_wait_ld();
-            if (sum && p.dg) *sum += dot16(stage, cl, v);
-            const uint4 w0 = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
-            const uint4 w1 = make_uint4(pack_bf2(v[8], v[9]), pack_bf2(v[10], v[11]), pack_bf2(v[12], v[13]), pack_bf2(v[14], v[15]));
-            if (Lc == C) {  // (each thread replaces the elements that it alone has read)
-                uint8_t *dst = sm + stage + (cl >> 6) * TILE;
-                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, cl & 63)) = w0;
-                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, (cl & 63) + 8)) = w1;
-            } else if (r < Lc && cl < d) {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + ((size_t)(row0 + r) * p.H + h) * d + cl);
-                dst[0] = w0;
-                dst[1] = w1;
+            for (int q = 0; q < 4; ++q) {
+                const uint4 w = make_uint4(pack_bf2(v[8 * q], v[8 * q + 1]), pack_bf2(v[8 * q + 2], v[8 * q + 3]),
+                                           pack_bf2(v[8 * q + 4], v[8 * q + 5]), pack_bf2(v[8 * q + 6], v[8 * q + 7]));
+                const int cl = col + 8 * q;
+                if (Lc == C)
+                    *reinterpret_cast<uint4 *>(sm + stage + (cl >> 6) * TILE + sw128_offset(r, cl & 63)) = w;
+                else if (r < Lc && cl < d)
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + ((size_t)(cur.row0 + r) * p.H + cur.h) * d + cl) = w;
             }
-        }
-    };
-    if (!bad) {
+        };
         wait(B_QK);
         tc_fence_after();
         if (ok && col < DKP) {
-            result(T2, L::Q, p.dq, p.dk, &rs);
-            result(T3, L::K, p.dk_, p.dk, &cs);
+            result(T2, L::stQ, p.dq, p.dk, L::Q, &rs);
+            result(T3, L::stK, p.dk_, p.dk, L::K, &cs);
         }
         if (p.dg) {
             red[grp * C + r] = rs;
@@ -915,15 +950,17 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         }
         fence_proxy_async_smem();
         bad = __syncthreads_or(!ok);
-    }
-    if (!bad) {
-        if (Lc == C && tid == 0) {
+        if (bad) break;
+        if (copier) {
+            if (Lc == C) {
 #pragma unroll
-            for (int b = 0; b < DKP / 64; ++b) {
-                tma_store_3d(&tm_dq, sm + L::Q + b * TILE, 64 * b, h, (int)row0);
-                tma_store_3d(&tm_dk, sm + L::K + b * TILE, 64 * b, h, (int)row0);
+                for (int b = 0; b < DKP / 64; ++b) {
+                    tma_store_3d(&tm_dq, sm + L::stQ + b * TILE, 64 * b, cur.h, (int)cur.row0);
+                    tma_store_3d(&tm_dk, sm + L::stK + b * TILE, 64 * b, cur.h, (int)cur.row0);
+                }
+                bulk_commit();
             }
-            bulk_commit();
+            if (more) load_qk(nxt, it + 1);
         }
         __syncwarp();
         // dg by one warp: what a token from t on reads of one before t. Within the chunk: the later rows' sums
@@ -954,34 +991,46 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 4 * lane + e;
-                if (i < Lc) st_elem(static_cast<__nv_bfloat16 *>(p.dg), (size_t)(row0 + i) * p.H + h, (float)(after + fb + through));
+                if (i < Lc) st_elem(static_cast<__nv_bfloat16 *>(p.dg), (size_t)(cur.row0 + i) * p.H + cur.h, (float)(after + fb + through));
                 after -= a[e];
                 fb += b[e];
             }
         }
         wait(B_V);
         tc_fence_after();
-        const uint32_t stage = L::over ? L::dA : L::V;
-        if (ok && col < DVP) result(T1, stage, p.dv_, p.dv, nullptr);
+        if (copier && ok && more) load_o(nxt);
+        __syncwarp();
+        if (ok && col < DVP) result(T1, L::stV, p.dv_, p.dv, 0, nullptr);
         fence_proxy_async_smem();
+        tc_fence_before();
         bad = __syncthreads_or(!ok);
-        if (!bad && Lc == C && tid == 0) {
+        if (bad) break;
+        if (copier) {
+            if (Lc == C) {
 #pragma unroll
-            for (int b = 0; b < DVP / 64; ++b) tma_store_3d(&tm_dv, sm + stage + b * TILE, 64 * b, h, (int)row0);
-            bulk_commit();
+                for (int b = 0; b < DVP / 64; ++b) tma_store_3d(&tm_dv, sm + L::stV + b * TILE, 64 * b, cur.h, (int)cur.row0);
+                bulk_commit();
+            }
+            bulk_wait_read_all();  // the staged results are read: their places may be loaded over
+            if (more) load_vsr(nxt);
+        }
+        __syncwarp();
+        if (!more) break;
+        cur = nxt;
+    }
+    if (bad) {  // leave nothing in flight behind: the copies, and whatever products were issued
+        if (copier) {
+            if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
+            bulk_wait_read_all();
+            for (int b = 0; b < 3; ++b)
+                if (loads[b] > 0) mbar_wait_bounded(bars + L_QK + b, (uint32_t)(loads[b] - 1) & 1u, kWaitCycles);
+        }
+        if (issuer) {
+            mma_commit(bars + B_END);
+            mbar_wait_bounded(bars + B_END, 0, kWaitCycles);
         }
     }
-    if (tid == 0) bulk_wait_read_all();
     tc_fence_before();
-    if (bad && tid == 0) {  // leave nothing in flight behind: the copies, and whatever products were issued
-        if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
-        mbar_wait_bounded(bars + L_QK, 0, kWaitCycles);
-        mbar_wait_bounded(bars + L_VO, 0, kWaitCycles);
-        mbar_wait_bounded(bars + L_SR, 0, kWaitCycles);
-        uint64_t *spare = bars + L_QK;  // its copies are done: a second phase, completed by the last product
-        mma_commit(spare);
-        mbar_wait_bounded(spare, 1, kWaitCycles);
-    }
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
@@ -1105,11 +1154,12 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     t.gates = s.gates;
     t.S = s.blob[0];
     t.R = s.blob[1];
-    t.ahead = device_sm_count();
+    t.tiles = units;
     const auto kern = hla_grad_tc_kernel<DKP, DVP>;
     constexpr size_t bytes = GradTile<DKP, DVP>::bytes;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) != cudaSuccess) return e;
-    kern<<<units, 512, bytes, a.stream>>>(m.q, m.k, m.v, m.o, m.dq, m.dk, m.dv, t);
+    const unsigned sms = (unsigned)device_sm_count();
+    kern<<<units < sms ? units : sms, 512, bytes, a.stream>>>(m.q, m.k, m.v, m.o, m.dq, m.dk, m.dv, t);
     return cudaGetLastError();
 }
 
