@@ -242,8 +242,9 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr uint32_t TX = 0, TO = 128, TS = 256, TP = 384;  // increment, outputs, scores, bf16 scores
 
     bool ok = true;
-    const auto wait = [&](int b, int i) {
+    const auto wait = [&](int b, int i) {  // (by a warp that goes on or gives up as one, or by one thread)
         if (ok) ok = mbar_wait_bounded(bars + b, (uint32_t)i & 1u, kWaitCycles);
+        if (warp < 16) ok = __all_sync(0xffffffffu, ok);
         return ok;
     };
     const auto wait_tile = [&](int b, int i) { return NS == 1 ? wait(b, i) : wait(b + (i & 1), i >> 1); };
@@ -378,7 +379,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 }
                 operand();
                 done(D_S);
-                if (tid == 256 && wait(D_S, i)) {
+                if (wait(D_S, i) && tid == 256) {
                     bulk_store(s.blob[dir] + ((size_t)(sp.slot + chunk(i)) * p.H + h) * blob_bytes(DKP, DVP), sm + L::S, DKP * DVP * 2);
                     bulk_commit();
                 }

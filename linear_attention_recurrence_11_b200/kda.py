@@ -9,6 +9,7 @@ pass them. There is no CPU fallback: importing this module raises if
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -575,32 +576,60 @@ def kda_kcp_scan(S0, M, Z, *, stream=None):
     return S_in, S_T
 
 
+# The single-token calls take the GPU two to four microseconds, so what they spend here counts: one test per tensor
+# (_need only says what is wrong with it), no context manager on the current device, plain integers as pointers.
+_NO_CONTEXT = contextlib.nullcontext()
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(dev, stream):
     """Device of the tensors and, when given, the call's stream made current: what is allocated inside belongs to
     the stream that the kernels run on, so that freeing it cannot hand it to another stream's work too early."""
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev)
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        return torch.cuda.stream(stream)
+    return _NO_CONTEXT if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _raw_stream(stream, dev):
+    return _current_raw_stream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _check(t, name, dtype, shape, dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _hla_gate(g, dtype, shape, dev):
     """KDA_HLA_GATE_*: g of the activations' type, one number per token and head, or fp32 ``[H]``."""
     if isinstance(g, torch.Tensor) and g.dim() == 1:
-        _need(g, "g", torch.float32, shape[-1:], dev)
+        _check(g, "g", torch.float32, shape[-1:], dev)
         return KDA_HLA_GATE_HEAD
-    _need(g, "g", dtype, shape, dev)
+    _check(g, "g", dtype, shape, dev)
     return KDA_HLA_GATE_TOKEN
 
 
-def _hla_shapes(q, k, v, g, cu_seqlens):
+def _hla_first(k, v, dims):
+    """The tensor that the others' type, device and sizes are taken from."""
     _need(k, "k")
-    dtype, dev = k.dtype, k.device
-    if dtype not in DTYPES:
-        raise ValueError(f"unsupported dtype {dtype}")
-    if k.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
-        raise ValueError("q, k and v are [B, T, H, d]")
+    if k.dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {k.dtype}")
+    if k.dim() != dims or not isinstance(v, torch.Tensor) or v.dim() != dims:
+        raise ValueError("q, k and v are [B, T, H, d]" if dims == 4 else "q, k and v are [N, H, d]")
+    return k.dtype, k.device, v.shape[-1]
+
+
+def _hla_shapes(q, k, v, g, cu_seqlens):
+    dtype, dev, dv = _hla_first(k, v, 4)
     B, T, H, dk = k.shape
-    dv = v.shape[-1]
-    _need(q, "q", dtype, (B, T, H, dk), dev)
-    _need(v, "v", dtype, (B, T, H, dv), dev)
+    _check(q, "q", dtype, (B, T, H, dk), dev)
+    _check(v, "v", dtype, (B, T, H, dv), dev)
     gate = _hla_gate(g, dtype, (B, T, H), dev)
     N = B
     if cu_seqlens is not None:
@@ -608,6 +637,8 @@ def _hla_shapes(q, k, v, g, cu_seqlens):
         if B != 1:
             raise ValueError("cu_seqlens needs B == 1")
         N = cu_seqlens.numel() - 1
+        if N < 1:
+            raise ValueError("cu_seqlens needs at least two offsets")
     return dtype, dev, B, T, H, dk, dv, gate, N
 
 
@@ -644,25 +675,25 @@ def kda_hla_forward(q, k, v, g, S0=None, *, scale: float = 1.0, cu_seqlens=None,
     Returns ``(o, S_T)`` (S_T None when ``return_state`` is False and none is given)."""
     dtype, dev, B, T, H, dk, dv, gate, N = _hla_shapes(q, k, v, g, cu_seqlens)
     if S0 is not None:
-        _need(S0, "S0", torch.float32, (N, H, dv, dk), dev)
-    with _on(dev, stream), torch.cuda.device(dev):
+        _check(S0, "S0", torch.float32, (N, H, dv, dk), dev)
+    with _on(dev, stream):
         if o is None:
             # tokens outside the sequences of a packed batch are not written
             o = torch.empty((B, T, H, dv), dtype=dtype, device=dev)
-        _need(o, "o", dtype, (B, T, H, dv), dev)
+        _check(o, "o", dtype, (B, T, H, dv), dev)
         if return_state and S_T is None:
             S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
         if S_T is not None:
-            _need(S_T, "S_T", torch.float32, (N, H, dv, dk), dev)
+            _check(S_T, "S_T", torch.float32, (N, H, dv, dk), dev)
         if dev_status is not None:
             _need(dev_status, "dev_status", torch.int32, None, dev)
         packed = N if cu_seqlens is not None else 0
         size = _lib.kda_hla_forward_workspace_size(B, T, H, dk, dv, packed, DTYPES[dtype], PATHS[path])
         workspace = _hla_workspace(size, workspace, dev, "kda_hla_forward")
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        rc = _lib.kda_hla_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(o), _ptr(S_T), B, T, H, dk, dv,
-                                  float(scale), DTYPES[dtype], gate, _ptr(cu_seqlens), packed, _ptr(workspace), ws_bytes,
-                                  _ptr(dev_status), _stream_handle(stream, dev), PATHS[path])
+        rc = _lib.kda_hla_forward(_addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(o), _addr(S_T), B, T, H, dk, dv,
+                                  float(scale), DTYPES[dtype], gate, _addr(cu_seqlens), packed, _addr(workspace), ws_bytes,
+                                  _addr(dev_status), _raw_stream(stream, dev), PATHS[path])
     if rc != KDA_OK:
         raise KdaError(rc, "kda_hla_forward")
     return o, S_T
@@ -675,13 +706,13 @@ def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, 
     ``return_dg`` is False, dS0 (fp32) is None when ``return_dS0`` is False. Rows outside the sequences of a packed
     batch are zero."""
     dtype, dev, B, T, H, dk, dv, gate, N = _hla_shapes(q, k, v, g, cu_seqlens)
-    _need(do, "do", dtype, (B, T, H, dv), dev)
+    _check(do, "do", dtype, (B, T, H, dv), dev)
     for name, x in (("S0", S0), ("dS_T", dS_T)):
         if x is not None:
-            _need(x, name, torch.float32, (N, H, dv, dk), dev)
+            _check(x, name, torch.float32, (N, H, dv, dk), dev)
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32, None, dev)
-    with _on(dev, stream), torch.cuda.device(dev):
+    with _on(dev, stream):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         dg = torch.empty_like(g) if gate == KDA_HLA_GATE_TOKEN and return_dg else None
         dS0 = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev) if return_dS0 else None
@@ -689,10 +720,10 @@ def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, 
         size = _lib.kda_hla_backward_workspace_size(B, T, H, dk, dv, packed, DTYPES[dtype], PATHS[path])
         workspace = _hla_workspace(size, workspace, dev, "kda_hla_backward")
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        rc = _lib.kda_hla_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(do), _ptr(dS_T), _ptr(dq), _ptr(dk_),
-                                   _ptr(dv_), _ptr(dg), _ptr(dS0), B, T, H, dk, dv, float(scale), DTYPES[dtype], gate,
-                                   _ptr(cu_seqlens), packed, _ptr(workspace), ws_bytes, _ptr(dev_status),
-                                   _stream_handle(stream, dev), PATHS[path])
+        rc = _lib.kda_hla_backward(_addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(do), _addr(dS_T), _addr(dq), _addr(dk_),
+                                   _addr(dv_), _addr(dg), _addr(dS0), B, T, H, dk, dv, float(scale), DTYPES[dtype], gate,
+                                   _addr(cu_seqlens), packed, _addr(workspace), ws_bytes, _addr(dev_status),
+                                   _raw_stream(stream, dev), PATHS[path])
     if rc != KDA_OK:
         raise KdaError(rc, "kda_hla_backward")
     return dq, dk_, dv_, dg, dS0
@@ -701,24 +732,19 @@ def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, 
 def kda_hla_decode_step(q, k, v, g, S, o=None, *, scale: float = 1.0, stream=None):
     """One token of the same recurrence per request. q, k ``[N, H, dk]``; v ``[N, H, dv]``; g ``[N, H]`` of the same
     type or fp32 ``[H]``; S ``[N, H, dv, dk]`` fp32 updated in place. Returns o."""
-    _need(k, "k")
-    dtype, dev = k.dtype, k.device
-    if dtype not in DTYPES:
-        raise ValueError(f"unsupported dtype {dtype}")
-    if k.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
-        raise ValueError("q, k and v are [N, H, d]")
+    dtype, dev, dv = _hla_first(k, v, 3)
     N, H, dk = k.shape
-    dv = v.shape[-1]
-    _need(q, "q", dtype, (N, H, dk), dev)
-    _need(v, "v", dtype, (N, H, dv), dev)
+    _check(q, "q", dtype, (N, H, dk), dev)
+    _check(v, "v", dtype, (N, H, dv), dev)
     gate = _hla_gate(g, dtype, (N, H), dev)
-    _need(S, "S", torch.float32, (N, H, dv, dk), dev)
-    with _on(dev, stream), torch.cuda.device(dev):
+    _check(S, "S", torch.float32, (N, H, dv, dk), dev)
+    with _on(dev, stream):
         if o is None:
             o = torch.empty((N, H, dv), dtype=dtype, device=dev)
-        _need(o, "o", dtype, (N, H, dv), dev)
-        rc = _lib.kda_hla_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(o), N, H, dk, dv, float(scale),
-                                      DTYPES[dtype], gate, _stream_handle(stream, dev))
+        else:
+            _check(o, "o", dtype, (N, H, dv), dev)
+        rc = _lib.kda_hla_decode_step(_addr(q), _addr(k), _addr(v), _addr(g), _addr(S), _addr(o), N, H, dk, dv, float(scale),
+                                      DTYPES[dtype], gate, _raw_stream(stream, dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_hla_decode_step")
     return o
@@ -789,18 +815,22 @@ def kda_rope(q, k, inv_freq, *, positions=None, interleaved: bool = False, mscal
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq is [rot_dim / 2]")
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise ValueError(f"positions has dtype {positions.dtype}, expected int32 or int64")
-        _need(positions, "positions", None, (B, T), dev)
-    with _on(dev, stream), torch.cuda.device(dev):
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        _need(q_out, "q_out", dtype, q.shape, dev)
+        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions is a tensor of int32 or int64")
+        _check(positions, "positions", positions.dtype, (B, T), dev)
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        else:
+            _check(q_out, "q_out", dtype, q.shape, dev)
         if k is not None:
-            k_out = torch.empty_like(k) if k_out is None else k_out
-            _need(k_out, "k_out", dtype, k.shape, dev)
-        rc = _lib.kda_rope(_ptr(q), _ptr(k), _ptr(positions), int(positions is not None and positions.dtype == torch.int64),
-                           _ptr(inv_freq), _ptr(q_out), _ptr(k_out), B, T, Hq, Hk, d, 2 * inv_freq.numel(),
-                           int(interleaved), int(inverse), float(mscale), DTYPES[dtype], _stream_handle(stream, dev))
+            if k_out is None:
+                k_out = torch.empty_like(k)
+            else:
+                _check(k_out, "k_out", dtype, k.shape, dev)
+        rc = _lib.kda_rope(_addr(q), _addr(k), _addr(positions), int(positions is not None and positions.dtype == torch.int64),
+                           _addr(inv_freq), _addr(q_out), _addr(k_out), B, T, Hq, Hk, d, 2 * inv_freq.numel(),
+                           int(interleaved), int(inverse), float(mscale), DTYPES[dtype], _raw_stream(stream, dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_rope")
     return q_out, k_out

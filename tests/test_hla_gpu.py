@@ -83,6 +83,9 @@ SHAPES = [  # B, T, H, dk, dv, dtype, gate, S0
     (1, 129, 2, 128, 128, "bf16", "head", True),
     (3, 300, 5, 128, 128, "bf16", "token", False),
     (1, 513, 3, 128, 128, "bf16", "token", True),
+    (2, 1290, 9, 128, 128, "bf16", "token", True),   # more chunks than SMs, partial ones among them
+    (3, 1030, 7, 64, 128, "bf16", "token", False),
+    (1, 2700, 9, 128, 64, "bf16", "head", True),
     (1, 1, 2, 32, 64, "f32", "token", True),
     (2, 97, 3, 64, 32, "f32", "head", True),
     (1, 200, 2, 128, 128, "f32", "token", False),
@@ -130,6 +133,14 @@ def test_packed(K, dtype, d, lead, tail):
         if name != "dS0":
             assert (a[:, :lead] == 0).all() and (a[:, cu[-1]:] == 0).all()
     assert torch.equal(got[4][2], x["dS_T"][2])
+
+
+def test_packed_more_chains_than_sms(K):
+    """Many short and a few long sequences: chains in order of length, chunks of all of them in one grid."""
+    lens = [5, 1, 0, 260, 128, 3, 7, 129, 0, 1, 64, 2, 90, 700, 1, 33, 256, 1, 1, 11]
+    x = inputs(1, sum(lens), 9, 128, 128, "bf16", seed=8, N=len(lens))
+    check_forward(K, x, "bf16", 0.5, cu_of(lens))
+    check_backward(K, x, "bf16", 0.5, cu_of(lens))
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 32)])
