@@ -185,11 +185,30 @@ __device__ __forceinline__ void hla_load_scan_gate(const HlaArgs &p, long long r
     hla_scan_gate(gate, G);
 }
 
+// Segments. A chain's chunks run one after another; where there are too few chains to fill the GPU, sequences are
+// cut into segments that run side by side, at the price of a pass for their end states, a scan over those, and two
+// launches.
+struct HlaSegments {
+    int sc = 0;                                  // chunks per segment; 0: whole sequences
+    float *state[2] = {nullptr, nullptr};        // per direction: [segment slot][H][dv][dk], end states, then start states
+    float *keep[2] = {nullptr, nullptr};         // per direction: decay over each segment [segment slot][H]
+};
+// Segment slot -> sequence and segment; false for a slot without one (an empty sequence keeps one segment, which
+// passes its state on).
+__device__ __forceinline__ bool hla_segment_of(const HlaArgs &p, long long slot, int tokens, int &n, int &sg) {
+    HlaSpan sp;
+    hla_chunk_of(p, slot, tokens, n, sg, sp);
+    return sg >= 0 && sg < max(1, sp.nch);
+}
+// Chunks per segment for `chains` chains on a GPU that runs `slots` of them at once. Both ways take as long as
+// chunks in a row: the whole sequence's, or twice a segment's and about half a dozen for the scan and the launches.
+int hla_segment_chunks(const HlaArgs &a, int C, long long chains, long long slots);
+cudaError_t launch_hla_segment_scan(const HlaArgs &a, const HlaSegments &s, int tokens, int dirs);
+
 // Launchers (return cudaSuccess or the launch error).
 cudaError_t launch_hla_forward_simt(const HlaArgs &a);
-size_t hla_forward_simt_workspace(const HlaArgs &a);
 cudaError_t launch_hla_backward_simt(const HlaArgs &a);
-size_t hla_backward_simt_workspace(const HlaArgs &a);
+size_t hla_simt_workspace(const HlaArgs &a, bool back);
 cudaError_t launch_hla_clear_outside(const HlaArgs &a);  // packed batches: zero gradients of rows of no sequence
 // the tensor-core kernels: bf16, every head size
 bool hla_tc_supported(const HlaArgs &a);

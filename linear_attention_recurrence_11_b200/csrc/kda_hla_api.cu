@@ -35,7 +35,7 @@ bool use_tc(const kda::HlaArgs &a, int path) { return path != KDA_PATH_SIMT && a
 
 size_t workspace_of(const kda::HlaArgs &a, bool back, int path) {
     if (use_tc(a, path)) return kda::hla_tc_workspace(a, back);
-    return back ? kda::hla_backward_simt_workspace(a) : kda::hla_forward_simt_workspace(a);
+    return kda::hla_simt_workspace(a, back);
 }
 
 }  // namespace

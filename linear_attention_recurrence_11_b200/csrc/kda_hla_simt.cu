@@ -1,12 +1,15 @@
-// Linear attention with one decay per head on CUDA cores (fp32 arithmetic, fp32 or bf16 storage,
-// any of the head sizes): prefill and its backward pass, in chunks of 64 tokens.
+// Linear attention with one decay per head in fp32 accuracy (fp32 or bf16 storage, any of the head sizes):
+// prefill and its backward pass, in chunks of 64 tokens. The chunked form is in kda_hla.cuh.
 //
-// Three kernels. The state kernel walks the chunks of a (sequence, head, 32 rows of dv) in order
-// and writes the state before each chunk (or, from the last chunk to the first, the state's
-// gradient behind it); the rows of S^T evolve independently, so the split over dv is exact. The
-// output and gradient kernels then take every chunk on its own, so that a few long sequences fill
-// the GPU. The chunked form is in kda_hla.cuh. What bounds them: the FFMA rate, fed from shared
-// memory by 4 x 8 (4 x 4, 4 x 2) register tiles of 16 x 16 threads.
+// Three kernels. The state kernel walks the chunks of a (sequence, head, 32 rows of dv) in order and writes the
+// state before each chunk (or, from the last chunk to the first, the state's gradient behind it); the rows of S^T
+// evolve independently, so the split over dv is exact, and where chains are few the sequences are cut into
+// segments. The output and gradient kernels then take every chunk on its own.
+//
+// Products: warp-level TF32 matrix instructions on operands split into two TF32 numbers each, x = hi + lo with 11 + 11
+// bits, as lo hi + hi lo + hi hi with fp32 accumulation: what is dropped is below 2^-21 of a product, the order of
+// fp32's own rounding. Measured against FFMA register tiles (4 x 8 per thread), the gradients of 16 heads x 2099
+// tokens take 0.4 of the time: a fragment's element is read from shared memory once for 8 to 32 products.
 #include "kda_hla.cuh"
 
 namespace kda {
@@ -14,78 +17,86 @@ namespace {
 
 constexpr int C = 64;
 constexpr int NT = 256;
-constexpr int JB = 32;  // dv rows of a state tile
-constexpr int LP = C + 4;
+constexpr int JB = 32;      // dv rows of a state tile
+constexpr int LP = C + 4;   // row strides are 4 mod 32 floats: the fragments' reads along rows hit all banks
 
-// ------------------------------------------------------ register-tiled products
-// c[i][j] += sum_k A(m, k) B(k, n) with m = ty + 16 i, n = tx + 16 j (tx, ty: this thread of 16 x 16).
-// nt: A[m][k], B[n][k] rows; nn: A[m][k], B[k][n]; tn: A[k][m], B[k][n]. Row strides are multiples
-// of four floats that are 4 mod 32, so that the 128-bit reads of eight consecutive rows hit all banks.
-template <int K, int NI, int NJ>
-__device__ __forceinline__ void mm_nt(float (&c)[NI][NJ], const float *A, int lda, const float *B, int ldb) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 4
-    for (int k = 0; k < K; k += 4) {
-        float4 a[NI], b[NJ];
+// ------------------------------------------------------------------ products
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;   // to nearest, in magnitude
+    lo = __float_as_uint(x - __uint_as_float(hi));       // (its low bits are ignored: 2^-10 of it)
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// A warp's part of a product: 32 rows from m0 on, and of every `step` columns 8 from n0 on. With g = lane / 4 and
+// t = lane % 4, c[i][j] holds rows m0 + 16 i + g (elements 0, 1) and + 8 (2, 3), columns n0 + step j + 2 t and + 1.
+struct WarpTile {
+    int m0, n0, g, t;
+    __device__ __forceinline__ int row(int i, int e) const { return m0 + 16 * i + g + 8 * (e >> 1); }
+    template <int kStep>
+    __device__ __forceinline__ int col(int j, int e) const { return n0 + kStep * j + 2 * t + (e & 1); }
+};
+// the 8 warps over 64 rows: 2 x 4, and columns in steps of 32
+__device__ __forceinline__ WarpTile tile_2x4() {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    return {32 * (warp >> 2), 8 * (warp & 3), lane >> 2, lane & 3};
+}
+
+// c += A B over K. A is [m][k], or with kAT [k][m]; B is [k][n], or with kBT [n][k]. The matrix instructions cut their
+// sums off instead of rounding them: over K = 128 that alone came to 3e-6 of the result. So 16 of K at a time are summed
+// by them, from zero, and added to c in fp32 (4e-7).
+template <int K, int NJ, int kStep, bool kAT, bool kBT>
+__device__ __forceinline__ void mm(float (&c)[2][NJ][4], const WarpTile &w, const float *A, int lda, const float *B, int ldb) {
+#pragma unroll 1
+    for (int kb = 0; kb < K; kb += 16) {
+        float sum[2][NJ][4];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * lda + k);
+        for (int kk = 0; kk < 16; kk += 8) {
+            const int k0 = kb + kk;
+            uint32_t ah[2][4], al[2][4];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + k);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+                for (int e = 0; e < 4; ++e) {
+                    const int m = w.m0 + 16 * i + w.g + 8 * (e & 1), k = k0 + w.t + 4 * (e >> 1);
+                    split_tf32(kAT ? A[k * lda + m] : A[m * lda + k], ah[i][e], al[i][e]);
+                }
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                c[i][j] = fmaf(a[i].x, b[j].x, c[i][j]);
-                c[i][j] = fmaf(a[i].y, b[j].y, c[i][j]);
-                c[i][j] = fmaf(a[i].z, b[j].z, c[i][j]);
-                c[i][j] = fmaf(a[i].w, b[j].w, c[i][j]);
-            }
-    }
-}
-template <int K, int NI, int NJ>
-__device__ __forceinline__ void mm_nn(float (&c)[NI][NJ], const float *A, int lda, const float *B, int ldb) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 2
-    for (int k = 0; k < K; k += 4) {
-        float4 a[NI];
+                uint32_t bh[2], bl[2];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) a[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * lda + k);
+                for (int e = 0; e < 2; ++e) {
+                    const int n = w.n0 + kStep * j + w.g, k = k0 + w.t + 4 * e;
+                    split_tf32(kBT ? B[n * ldb + k] : B[k * ldb + n], bh[e], bl[e]);
+                }
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            float b[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) b[j] = B[(k + kk) * ldb + tx + 16 * j];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const float x = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) c[i][j] = fmaf(x, b[j], c[i][j]);
+                for (int i = 0; i < 2; ++i) {
+                    if (kk == 0) sum[i][j][0] = sum[i][j][1] = sum[i][j][2] = sum[i][j][3] = 0.f;
+                    mma_tf32(sum[i][j], al[i], bh);
+                    mma_tf32(sum[i][j], ah[i], bl);
+                    mma_tf32(sum[i][j], ah[i], bh);
+                }
             }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[i][j][e] += sum[i][j][e];
     }
 }
-template <int K, int NI, int NJ>
-__device__ __forceinline__ void mm_tn(float (&c)[NI][NJ], const float *A, int lda, const float *B, int ldb) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 4
-    for (int k = 0; k < K; ++k) {
-        float a[NI], b[NJ];
+template <int NJ>
+__device__ __forceinline__ void zero(float (&c)[2][NJ][4]) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) a[i] = A[k * lda + ty + 16 * i];
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) b[j] = B[k * ldb + tx + 16 * j];
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) c[i][j] = fmaf(a[i], b[j], c[i][j]);
-    }
-}
-template <int NI, int NJ>
-__device__ __forceinline__ void zero(float (&c)[NI][NJ]) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) c[i][j] = 0.f;
+            for (int e = 0; e < 4; ++e) c[i][j][e] = 0.f;
 }
 
 // four consecutive elements (8- or 16-byte aligned)
@@ -96,98 +107,174 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
     const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&r.y));
     return make_float4(x.x, x.y, y.x, y.y);
 }
+__device__ __forceinline__ void st2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+}
 
-// rows [row0, row0 + Lc) of columns [c0, c0 + W) of a [tokens, H, D] tensor, times `scale`; zeros from Lc on
+// Columns [c0, c0 + W) of a chunk's rows of a [tokens, H, D] tensor, in two steps: read into registers (zeros from row
+// Lc on), and written to shared memory.
 template <typename Tin, int D, int W>
-__device__ __forceinline__ void load_tile(float *s, int lds, const void *src, long long row0, int H, int h, int c0, int Lc,
-                                          float scale = 1.f) {
-    const Tin *p = static_cast<const Tin *>(src);
-#pragma unroll 4
-    for (int idx = threadIdx.x; idx < C * (W / 4); idx += NT) {
-        const int r = idx / (W / 4), c = 4 * (idx % (W / 4));
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < Lc) x = ld4(p + ((size_t)(row0 + r) * H + h) * D + c0 + c);
-        *reinterpret_cast<float4 *>(s + r * lds + c) = make_float4(scale * x.x, scale * x.y, scale * x.z, scale * x.w);
+struct TileRegs {
+    static constexpr int N = (C * (W / 4) + NT - 1) / NT;
+    float4 x[N];
+    __device__ __forceinline__ void load(const void *src, long long row0, int H, int h, int c0, int Lc) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int idx = threadIdx.x + NT * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < Lc) x[i] = ld4(static_cast<const Tin *>(src) + ((size_t)(row0 + r) * H + h) * D + c0 + c);
+        }
     }
+    template <typename F>
+    __device__ __forceinline__ void store(float *s, int lds, F f) const {  // f(row): a factor
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int idx = threadIdx.x + NT * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
+            const float y = f(r);
+            if (r < C) *reinterpret_cast<float4 *>(s + r * lds + c) = make_float4(y * x[i].x, y * x[i].y, y * x[i].z, y * x[i].w);
+        }
+    }
+};
+template <typename Tin, int D, int W>
+__device__ __forceinline__ void load_tile(float *s, int lds, const void *src, long long row0, int H, int h, int c0, int Lc, float scale = 1.f) {
+    TileRegs<Tin, D, W> t;
+    t.load(src, row0, H, h, c0, Lc);
+    t.store(s, lds, [&](int) { return scale; });
 }
 
 // ------------------------------------------------------------------- states
-// kRev = false: X = the state; a = k, b = v, row weights e^{G_C - G_s}; chunks in order; start S0, end S_T.
-// kRev = true:  X = its gradient; a = q, b = dO, row weights scale e^{G_r}; chunks from the last to the
-//               first; start dS_T, end dS0.
-// X before each step goes to Xc [slot][H][DV][DK]. One CTA: 32 rows of dv; thread (lane, warp) holds
-// rows 4 warp .. + 3 and columns lane + 32 c.
-template <typename Tin, int DK, int DV, bool kRev>
-__global__ void __launch_bounds__(NT) hla_state_simt_kernel(const HlaArgs p, float *__restrict__ Xc) {
-    constexpr int NC = DK / 32;
-    __shared__ __align__(16) float sA[C * DK];
-    __shared__ __align__(16) float sB[C * JB];
+// Direction 0: X = the state; a = k, b = v, row weights e^{G_C - G_s}; chunks in order; start S0, end S_T.
+// Direction 1: X = its gradient; a = q, b = dO, row weights scale e^{G_r}; chunks from the last to the first; start
+// dS_T, end dS0. X before each step goes to X[dir] [slot][H][DV][DK]. With segments (sc > 0), a first launch (ends)
+// writes each segment's end state from zero, and the second starts from the segments' start states.
+struct StateArgs {
+    HlaArgs a;
+    float *X[2];
+    HlaSegments seg;
+    bool ends;
+};
+
+template <typename Tin, int DK, int DV>
+__global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
+    constexpr int KP = DK + 8, VP = JB + 8;  // (read down the columns: 8 mod 32)
+    constexpr int WN = DK < 64 ? 4 : 8, NJ = DK / (8 * WN);
+    const HlaArgs &p = s.a;
+    __shared__ __align__(16) float sA[C * KP];
+    __shared__ __align__(16) float sB[C * VP];
     __shared__ float2 G[C];
-    const int h = blockIdx.x % p.H, n = blockIdx.x / p.H, j0 = blockIdx.y * JB;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const HlaSpan sp = hla_span(p, n, C);
-    const float *start = kRev ? p.dST : p.S0;
-    float *end = kRev ? p.dS0 : p.ST;
-    const size_t sbase = ((size_t)n * p.H + h) * (size_t)(DV * DK);
+    const int dir = blockIdx.z, j0 = blockIdx.y * JB, h = blockIdx.x % p.H;
+    const long long su = blockIdx.x / p.H;
+    int n = (int)su, sg = 0;
+    HlaSpan sp;
+    if (s.seg.sc && !hla_segment_of(p, su, s.seg.sc * C, n, sg)) return;
+    sp = hla_span(p, n, C);
+    const int nseg = s.seg.sc ? max(1, (sp.nch + s.seg.sc - 1) / s.seg.sc) : 1;
+    const int c0 = s.seg.sc ? sg * s.seg.sc : 0, c1 = s.seg.sc ? min(sp.nch, c0 + s.seg.sc) : sp.nch, nc = c1 - c0;
+    const bool last = dir ? sg == 0 : sg == nseg - 1;
+    if (s.ends && last) return;
+    const size_t base_n = ((size_t)n * p.H + h) * (size_t)(DV * DK), base_s = ((size_t)su * p.H + h) * (size_t)(DV * DK);
+    const float *start = s.ends ? nullptr : s.seg.sc ? s.seg.state[dir] + base_s : dir ? p.dST : p.S0;
+    if (start && !s.seg.sc) start += base_n;
+    float *end = s.ends ? s.seg.state[dir] + base_s : !last ? nullptr : dir ? p.dS0 : p.ST;
+    if (end && !s.ends) end += base_n;
 
-    float x[4][NC];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WarpTile w{0, 8 * (warp % WN), lane >> 2, lane & 3};
+    const bool active = warp < WN;
+    float x[2][NJ][4];
+    const auto each = [&](auto f) {  // (pairs of columns)
+        if (active)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            x[i][c] = start ? start[sbase + (size_t)(j0 + 4 * warp + i) * DK + lane + 32 * c] : 0.f;
-
-    for (int cc = 0; cc < sp.nch; ++cc) {
-        const int c = kRev ? sp.nch - 1 - cc : cc;
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) f((size_t)(j0 + w.row(i, e)) * DK + w.col<8 * WN>(j, e), x[i][j][e], x[i][j][e + 1]);
+    };
+    zero(x);
+    if (start) each([&](size_t at, float &u, float &v) {
+        const float2 y = *reinterpret_cast<const float2 *>(start + at);
+        u = y.x;
+        v = y.y;
+    });
+    const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
+    TileRegs<Tin, DK, DK> ta;
+    TileRegs<Tin, DV, JB> tb;
+    HlaGate<Tin, C> gate;
+    const auto load = [&](int i) {
+        const int c = chunk(i), Lc = min(C, sp.len - c * C);
         const long long row0 = sp.t0 + (long long)c * C;
-        const int Lc = min(C, sp.len - c * C);
-        float *dst = Xc + ((size_t)(sp.slot + c) * p.H + h) * (size_t)(DV * DK);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int cx = 0; cx < NC; ++cx) dst[(size_t)(j0 + 4 * warp + i) * DK + lane + 32 * cx] = x[i][cx];
-        __syncthreads();  // the previous chunk's tiles are consumed
-        if (warp == 0) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
-        load_tile<Tin, DK, DK>(sA, DK, kRev ? p.q : p.k, row0, p.H, h, 0, Lc);
-        load_tile<Tin, DV, JB>(sB, JB, kRev ? p.dO : p.v, row0, p.H, h, j0, Lc);
-        __syncthreads();
-        const float2 gC = G[C - 1];
-        const float2 g0 = make_float2(0.f, 0.f);
-        for (int idx = threadIdx.x; idx < C * JB; idx += NT) {
-            const float2 gr = G[idx / JB];
-            sB[idx] *= kRev ? p.scale * hla_decay(gr, g0) : hla_decay(gC, gr);
+        if (warp == 0) gate.load(p, row0, h, Lc);
+        ta.load(dir ? p.q : p.k, row0, p.H, h, 0, Lc);
+        tb.load(dir ? p.dO : p.v, row0, p.H, h, j0, Lc);
+    };
+    float total = 1.f;
+    if (nc > 0) load(0);
+    for (int i = 0; i < nc; ++i) {
+        if (!s.ends) {
+            float *dst = s.X[dir] + ((size_t)(sp.slot + chunk(i)) * p.H + h) * (size_t)(DV * DK);
+            each([&](size_t at, float &u, float &v) { *reinterpret_cast<float2 *>(dst + at) = make_float2(u, v); });
         }
+        if (warp == 0) hla_scan_gate(gate, G);
+        ta.store(sA, KP, [&](int) { return 1.f; });
         __syncthreads();
+        const float2 g0 = make_float2(0.f, 0.f), gC = G[C - 1];
+        tb.store(sB, VP, [&](int r) { return r >= C ? 0.f : dir ? p.scale * hla_decay(G[r], g0) : hla_decay(gC, G[r]); });
         const float keep = hla_decay(gC, g0);
+        total *= keep;
+        __syncthreads();
+        if (i + 1 < nc) load(i + 1);  // on its way while this one is multiplied
+        if (active) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
-            for (int cx = 0; cx < NC; ++cx) x[i][cx] *= keep;
-#pragma unroll 8
-        for (int s = 0; s < C; ++s) {
-            const float4 b = *reinterpret_cast<const float4 *>(sB + s * JB + 4 * warp);
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int cx = 0; cx < NC; ++cx) {
-                const float a = sA[s * DK + lane + 32 * cx];
-                x[0][cx] = fmaf(b.x, a, x[0][cx]);
-                x[1][cx] = fmaf(b.y, a, x[1][cx]);
-                x[2][cx] = fmaf(b.z, a, x[2][cx]);
-                x[3][cx] = fmaf(b.w, a, x[3][cx]);
-            }
+                    for (int e = 0; e < 4; ++e) x[a][j][e] *= keep;
+            mm<C, NJ, 8 * WN, true, false>(x, w, sB, VP, sA, KP);
         }
+        __syncthreads();  // the tiles are consumed
     }
-    if (end) {
+    if (end) each([&](size_t at, float &u, float &v) { *reinterpret_cast<float2 *>(end + at) = make_float2(u, v); });
+    if (s.ends && j0 == 0 && threadIdx.x == 0) s.seg.keep[dir][su * p.H + h] = total;
+}
+
+// End states of the segments -> their start states: start_0 = S0, start_{i+1} = keep_i start_i + end_i (in the
+// direction's order), in place, one thread per four elements of a (sequence, head). `tokens` per segment.
+__global__ void __launch_bounds__(256) hla_segment_scan_kernel(const HlaArgs p, const HlaSegments s, int tokens) {
+    constexpr int U = 8;  // end states on their way at once
+    const int dir = blockIdx.z, h = blockIdx.x % p.H, n = blockIdx.x / p.H;
+    const int at = 4 * (blockIdx.y * 256 + threadIdx.x), size = p.dv * p.dk;
+    if (at >= size) return;
+    const HlaSpan sp = hla_span(p, n, tokens);
+    const int nseg = max(1, sp.nch);
+    const float *first = dir ? p.dST : p.S0;
+    float4 x = first ? *reinterpret_cast<const float4 *>(first + ((size_t)n * p.H + h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto where = [&](int i) { return (size_t)(sp.slot + (dir ? nseg - 1 - i : i)) * p.H + h; };
+    for (int i0 = 0; i0 < nseg; i0 += U) {
+        float4 e[U];
+        float keep[U];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < U; ++j)
+            if (i0 + j + 1 < nseg) {  // (the last segment's end is the sequence's: it has no slot)
+                e[j] = *reinterpret_cast<const float4 *>(s.state[dir] + where(i0 + j) * size + at);
+                keep[j] = s.keep[dir][where(i0 + j)];
+            }
 #pragma unroll
-            for (int c = 0; c < NC; ++c) end[sbase + (size_t)(j0 + 4 * warp + i) * DK + lane + 32 * c] = x[i][c];
+        for (int j = 0; j < U; ++j)
+            if (i0 + j < nseg) {
+                *reinterpret_cast<float4 *>(s.state[dir] + where(i0 + j) * size + at) = x;
+                if (i0 + j + 1 < nseg)
+                    x = make_float4(fmaf(keep[j], x.x, e[j].x), fmaf(keep[j], x.y, e[j].y), fmaf(keep[j], x.z, e[j].z), fmaf(keep[j], x.w, e[j].w));
+            }
     }
 }
 
 // ------------------------------------------------------------------ outputs
 template <int DK, int DV>
 struct OutSmem {
-    static constexpr int KP = DK + 4, VP = DV + 4;
+    static constexpr int KP = DK + 4, VP = DV + 8;
     // K's tile takes the state's tiles (JB rows of DK) once Q K^T is done
     static constexpr int floats = 2 * C * KP + C * VP + C * LP;
     static constexpr size_t bytes = sizeof(float) * floats + sizeof(float2) * C;
@@ -196,6 +283,7 @@ struct OutSmem {
 template <typename Tin, int DK, int DV>
 __global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const float *__restrict__ Sc) {
     using L = OutSmem<DK, DV>;
+    constexpr int VJ = DV / 32;
     extern __shared__ __align__(16) float smem[];
     float *sQ = smem, *sK = sQ + C * L::KP, *sV = sK + C * L::KP, *sP = sV + C * L::VP;
     float2 *G = reinterpret_cast<float2 *>(sP + C * LP);
@@ -206,73 +294,86 @@ __global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const
     if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
     const long long row0 = sp.t0 + (long long)c * C;
     const int Lc = min(C, sp.len - c * C);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const WarpTile w = tile_2x4();
     const bool has_state = c > 0 || p.S0 != nullptr;
 
-    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
     load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc, p.scale);
     load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
+    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
     __syncthreads();
     {
-        float a[4][4];
+        float a[2][2][4];
         zero(a);
-        mm_nt<DK>(a, sQ, L::KP, sK, L::KP);
+        mm<DK, 2, 32, false, true>(a, w, sQ, L::KP, sK, L::KP);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = ty + 16 * i, s = tx + 16 * j;
-                sP[r * LP + s] = s <= r ? a[i][j] * hla_decay(G[r], G[s]) : 0.f;
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int r = w.row(i, e), s = w.col<32>(j, e);
+                    *reinterpret_cast<float2 *>(sP + r * LP + s) =
+                        make_float2(s <= r ? a[i][j][e] * hla_decay(G[r], G[s]) : 0.f, s + 1 <= r ? a[i][j][e + 1] * hla_decay(G[r], G[s + 1]) : 0.f);
+                }
     }
     __syncthreads();  // P is written, K's tile is free
-    float acc[4][DV / 16];
+    float acc[2][VJ][4];
     zero(acc);
     if (has_state) {
         const float *S = Sc + ((size_t)slot * p.H + h) * (size_t)(DV * DK);
+        constexpr int JT = DV < 64 ? DV : 64;  // rows of the state at a time
 #pragma unroll
-        for (int jb = 0; jb < DV / JB; ++jb) {
-            for (int idx = threadIdx.x; idx < JB * (DK / 4); idx += NT) {
+        for (int jb = 0; jb < DV / JT; ++jb) {
+            for (int idx = threadIdx.x; idx < JT * (DK / 4); idx += NT) {
                 const int r = idx / (DK / 4), cc = 4 * (idx % (DK / 4));
-                *reinterpret_cast<float4 *>(sK + r * L::KP + cc) = ld4(S + (size_t)(jb * JB + r) * DK + cc);
+                *reinterpret_cast<float4 *>(sK + r * L::KP + cc) = ld4(S + (size_t)(jb * JT + r) * DK + cc);
             }
             __syncthreads();
-            float part[4][2];
+            float part[2][JT / 32][4];
             zero(part);
-            mm_nt<DK>(part, sQ, L::KP, sK, L::KP);
+            mm<DK, JT / 32, 32, false, true>(part, w, sQ, L::KP, sK, L::KP);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[i][2 * jb] = part[i][0];
-                acc[i][2 * jb + 1] = part[i][1];
-            }
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < JT / 32; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][jb * (JT / 32) + j][e] = part[i][j][e];
             __syncthreads();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float since = hla_decay(G[ty + 16 * i], make_float2(0.f, 0.f));
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < DV / 16; ++j) acc[i][j] *= since;
-        }
+            for (int e = 0; e < 4; e += 2) {
+                const float since = hla_decay(G[w.row(i, e)], make_float2(0.f, 0.f));
+#pragma unroll
+                for (int j = 0; j < VJ; ++j) {
+                    acc[i][j][e] *= since;
+                    acc[i][j][e + 1] *= since;
+                }
+            }
     }
-    mm_nn<C>(acc, sP, LP, sV, L::VP);
+    mm<C, VJ, 32, false, false>(acc, w, sP, LP, sV, L::VP);
     Tin *o = static_cast<Tin *>(p.o);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        if (r >= Lc) continue;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < DV / 16; ++j) st_elem(o, ((size_t)(row0 + r) * p.H + h) * DV + tx + 16 * j, acc[i][j]);
-    }
+        for (int e = 0; e < 4; e += 2) {
+            const int r = w.row(i, e);
+            if (r >= Lc) continue;
+#pragma unroll
+            for (int j = 0; j < VJ; ++j)
+                st2(o + ((size_t)(row0 + r) * p.H + h) * DV + w.col<32>(j, e), acc[i][j][e], acc[i][j][e + 1]);
+        }
 }
 
 // ---------------------------------------------------------------- gradients
 template <int DK, int DV>
 struct GradSmem {
     static constexpr int KP = DK + 4, VP = DV + 4;
-    // the last C x LP tile holds the state's tiles (JB x KP each) first, then the terms of dg
+    // the last tile holds the state's tiles (JB x KP each) first, then the pairs of dg
     static constexpr int XT = (2 * JB * KP > C * LP) ? 2 * JB * KP : C * LP;
-    static constexpr int floats = 2 * C * KP + 2 * C * VP + 2 * C * LP + XT + 4 * C + 32;
+    static constexpr int floats = 2 * C * KP + 2 * C * VP + 2 * C * LP + XT + 2 * 4 * C + C + 32;
     static constexpr size_t bytes = sizeof(float) * floats + sizeof(float2) * C;
 };
 
@@ -280,12 +381,12 @@ template <typename Tin, int DK, int DV>
 __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, const float *__restrict__ Sc,
                                                            const float *__restrict__ Rc) {
     using L = GradSmem<DK, DV>;
-    constexpr int KJ = DK / 16, VJ = DV / 16;
+    constexpr int KJ = DK / 32, VJ = DV / 32;
     extern __shared__ __align__(16) float smem[];
     float *sQ = smem, *sK = sQ + C * L::KP, *sV = sK + C * L::KP, *sO = sV + C * L::VP;
     float *sA = sO + C * L::VP, *sD = sA + C * LP, *sX = sD + C * LP;
-    float *sRead = sX + L::XT, *sWrit = sRead + C, *sWith = sWrit + C, *sThr = sWith + C;
-    float2 *G = reinterpret_cast<float2 *>(sThr + C + 32);
+    float *sRead = sX + L::XT, *sWrit = sRead + 4 * C, *sWith = sWrit + 4 * C, *sThr = sWith + C;  // (read, written: by column warp)
+    float2 *G = reinterpret_cast<float2 *>(sThr + 32);
     const int h = blockIdx.x % p.H;
     const long long slot = blockIdx.x / p.H;
     int n, c;
@@ -293,25 +394,24 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
     if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
     const long long row0 = sp.t0 + (long long)c * C;
     const int Lc = min(C, sp.len - c * C);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wn = warp & 3;
+    const WarpTile w = tile_2x4();
     const float2 g0 = make_float2(0.f, 0.f);
 
-    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
     load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc);
     load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sO, L::VP, p.dO, row0, p.H, h, 0, Lc, p.scale);
+    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
     __syncthreads();
 
     // the parts that go through the states: dQ from S_in, dK and dV from R, and their terms of dg
-    float dq[4][KJ], dk[4][KJ];
+    float dq[2][KJ][4], dk[2][KJ][4], dv[2][VJ][4];
     zero(dq);
     zero(dk);
     float thr = 0.f;
     const size_t xb = ((size_t)slot * p.H + h) * (size_t)(DV * DK);
     float *sS = sX, *sR = sX + JB * L::KP;
-    Tin *out_v = static_cast<Tin *>(p.dv_);
-    float dv[4][VJ];
 #pragma unroll
     for (int jb = 0; jb < DV / JB; ++jb) {
         for (int idx = threadIdx.x; idx < JB * (DK / 4); idx += NT) {
@@ -322,83 +422,94 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
             thr = fmaf(s4.x, r4.x, fmaf(s4.y, r4.y, fmaf(s4.z, r4.z, fmaf(s4.w, r4.w, thr))));
         }
         __syncthreads();
-        mm_nn<JB>(dq, sO + jb * JB, L::VP, sS, L::KP);
-        mm_nn<JB>(dk, sV + jb * JB, L::VP, sR, L::KP);
-        float part[4][2];
+        mm<JB, KJ, 32, false, false>(dq, w, sO + jb * JB, L::VP, sS, L::KP);
+        mm<JB, KJ, 32, false, false>(dk, w, sV + jb * JB, L::VP, sR, L::KP);
+        float part[2][1][4];
         zero(part);
-        mm_nt<DK>(part, sK, L::KP, sR, L::KP);
+        mm<DK, 1, 32, false, true>(part, w, sK, L::KP, sR, L::KP);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            dv[i][2 * jb] = part[i][0];
-            dv[i][2 * jb + 1] = part[i][1];
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dv[i][jb][e] = part[i][0][e];
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        const float since = hla_decay(G[r], g0), until = hla_decay(G[C - 1], G[r]);
-        float rd = 0.f, wr = 0.f;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-            dq[i][j] *= since;
-            dk[i][j] *= until;
-            rd = fmaf(dq[i][j], sQ[r * L::KP + tx + 16 * j], rd);
-            wr = fmaf(dk[i][j], sK[r * L::KP + tx + 16 * j], wr);
-        }
+        for (int e = 0; e < 4; e += 2) {
+            const int r = w.row(i, e);
+            const float since = hla_decay(G[r], g0), until = hla_decay(G[C - 1], G[r]);
+            float rd = 0.f, wr = 0.f;
 #pragma unroll
-        for (int j = 0; j < VJ; ++j) dv[i][j] *= until;
+            for (int j = 0; j < KJ; ++j)
 #pragma unroll
-        for (int off = 1; off < 16; off <<= 1) {
-            rd += __shfl_xor_sync(0xffffffffu, rd, off);
-            wr += __shfl_xor_sync(0xffffffffu, wr, off);
+                for (int k = 0; k < 2; ++k) {
+                    float &a = dq[i][j][e + k], &b = dk[i][j][e + k];
+                    a *= since;
+                    b *= until;
+                    rd = fmaf(a, sQ[r * L::KP + w.col<32>(j, e + k)], rd);
+                    wr = fmaf(b, sK[r * L::KP + w.col<32>(j, e + k)], wr);
+                }
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) {
+                dv[i][j][e] *= until;
+                dv[i][j][e + 1] *= until;
+            }
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) {
+                rd += __shfl_xor_sync(0xffffffffu, rd, off);
+                wr += __shfl_xor_sync(0xffffffffu, wr, off);
+            }
+            if (w.t == 0) {
+                sRead[wn * C + r] = rd;
+                sWrit[wn * C + r] = wr;
+            }
         }
-        if (tx == 0) {
-            sRead[r] = rd;
-            sWrit[r] = wr;
-        }
-    }
 #pragma unroll
     for (int off = 16; off; off >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, off);
     if (lane == 0) sThr[warp] = thr;
 
     // A = Q K^T . D, dA = dO' V^T . D, and the pairs within the chunk E = A . dO' V^T below the diagonal
     {
-        float a[4][4], da[4][4];
+        float a[2][2][4], da[2][2][4];
         zero(a);
         zero(da);
-        mm_nt<DK>(a, sQ, L::KP, sK, L::KP);
-        mm_nt<DV>(da, sO, L::VP, sV, L::VP);
+        mm<DK, 2, 32, false, true>(a, w, sQ, L::KP, sK, L::KP);
+        mm<DV, 2, 32, false, true>(da, w, sO, L::VP, sV, L::VP);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = ty + 16 * i, s = tx + 16 * j;
-                const float d = hla_decay(G[r], G[s]);
-                const float x = s <= r ? a[i][j] * d : 0.f;
-                sA[r * LP + s] = x;
-                sD[r * LP + s] = s <= r ? da[i][j] * d : 0.f;
-                sX[r * LP + s] = s < r ? x * da[i][j] : 0.f;
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = w.row(i, e), s = w.col<32>(j, e);
+                    const float d = hla_decay(G[r], G[s]);
+                    const float x = s <= r ? a[i][j][e] * d : 0.f;
+                    sA[r * LP + s] = x;
+                    sD[r * LP + s] = s <= r ? da[i][j][e] * d : 0.f;
+                    sX[r * LP + s] = s < r ? x * da[i][j][e] : 0.f;
+                }
     }
     __syncthreads();
-    mm_nn<C>(dq, sD, LP, sK, L::KP);
-    mm_tn<C>(dk, sD, LP, sQ, L::KP);
-    mm_tn<C>(dv, sA, LP, sO, L::VP);
-    Tin *out_q = static_cast<Tin *>(p.dq), *out_k = static_cast<Tin *>(p.dk_);
+    mm<C, KJ, 32, false, false>(dq, w, sD, LP, sK, L::KP);
+    mm<C, KJ, 32, true, false>(dk, w, sD, LP, sQ, L::KP);
+    mm<C, VJ, 32, true, false>(dv, w, sA, LP, sO, L::VP);
+    Tin *out_q = static_cast<Tin *>(p.dq), *out_k = static_cast<Tin *>(p.dk_), *out_v = static_cast<Tin *>(p.dv_);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        if (r >= Lc) continue;
-        const size_t row = (size_t)(row0 + r) * p.H + h;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) {
-            st_elem(out_q, row * DK + tx + 16 * j, dq[i][j]);
-            st_elem(out_k, row * DK + tx + 16 * j, dk[i][j]);
+        for (int e = 0; e < 4; e += 2) {
+            const int r = w.row(i, e);
+            if (r >= Lc) continue;
+            const size_t row = (size_t)(row0 + r) * p.H + h;
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                st2(out_q + row * DK + w.col<32>(j, e), dq[i][j][e], dq[i][j][e + 1]);
+                st2(out_k + row * DK + w.col<32>(j, e), dk[i][j][e], dk[i][j][e + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) st2(out_v + row * DV + w.col<32>(j, e), dv[i][j][e], dv[i][j][e + 1]);
         }
-#pragma unroll
-        for (int j = 0; j < VJ; ++j) st_elem(out_v, row * DV + tx + 16 * j, dv[i][j]);
-    }
     if (!p.dg) return;
 
     // dg: suffix sums of E down each column, then row sums left of the diagonal; plus the suffix sums of
@@ -406,7 +517,8 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
     if (threadIdx.x < C) {
         const int s = threadIdx.x;
         float u = 0.f;
-        for (int r = C - 1; r > s; --r) {
+#pragma unroll 8
+        for (int r = C - 1; r >= 0; --r) {  // (E is zero on and above the diagonal)
             u += sX[r * LP + s];
             sX[r * LP + s] = u;
         }
@@ -422,16 +534,31 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
         if (tx == 0) sWith[t] = u;
     }
     __syncthreads();
-    if (threadIdx.x < C) {
-        const int t = threadIdx.x;
-        float rd = 0.f, wr = 0.f, through = 0.f;
-        for (int r = C - 1; r >= t; --r) rd += sRead[r];
-        for (int s = 0; s < t; ++s) wr += sWrit[s];
+    if (threadIdx.x < 32) {  // two tokens a lane
+        const int t = 2 * lane;
+        float rd[2], wr[2], through = 0.f;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) through += sThr[w];
-        if (t < Lc)
-            st_elem(static_cast<Tin *>(p.dg), (size_t)(row0 + t) * p.H + h,
-                    (sWith[t] + rd) + fmaf(hla_decay(G[C - 1], g0), through, wr));
+        for (int k = 0; k < 2; ++k) {
+            rd[k] = (sRead[t + k] + sRead[C + t + k]) + (sRead[2 * C + t + k] + sRead[3 * C + t + k]);
+            wr[k] = (sWrit[t + k] + sWrit[C + t + k]) + (sWrit[2 * C + t + k] + sWrit[3 * C + t + k]);
+        }
+        float after = rd[0] + rd[1], before = wr[0] + wr[1];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float y = __shfl_down_sync(0xffffffffu, after, off), z = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane + off < 32) after += y;
+            if (lane >= off) before += z;
+        }
+        // (exclusive sums are shifted, not subtracted: a difference would lose what is small)
+        float later = __shfl_down_sync(0xffffffffu, after, 1), earlier = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 31) later = 0.f;
+        if (lane == 0) earlier = 0.f;
+#pragma unroll
+        for (int k = 0; k < NT / 32; ++k) through += sThr[k];
+        through *= hla_decay(G[C - 1], g0);
+        Tin *dg = static_cast<Tin *>(p.dg);
+        if (t < Lc) st_elem(dg, (size_t)(row0 + t) * p.H + h, (sWith[t] + ((rd[0] + rd[1]) + later)) + (earlier + through));
+        if (t + 1 < Lc) st_elem(dg, (size_t)(row0 + t + 1) * p.H + h, (sWith[t + 1] + (rd[1] + later)) + ((earlier + wr[0]) + through));
     }
 }
 
@@ -461,37 +588,81 @@ cudaError_t with_smem(F kern, size_t bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Workspace: per direction the states at the chunks' borders, and, with segments, the segments' states and decays.
+struct Layout {
+    int sc;
+    long long slots, seg_slots;
+    size_t X[2], seg[2], keep[2], bytes;
+};
+Layout layout(const HlaArgs &a, bool back) {
+    Layout l{};
+    const int dirs = back ? 2 : 1;
+    const bool packed = a.cu_seqlens != nullptr;
+    // up to four state CTAs run on an SM
+    l.sc = hla_segment_chunks(a, C, (long long)a.N * a.H * (a.dv / JB) * dirs, 4LL * device_sm_count());
+    l.slots = hla_slots(packed, a.N, a.T, C);
+    l.seg_slots = l.sc ? hla_slots(packed, a.N, a.T, l.sc * C) : 0;
+    size_t at = 0;
+    const auto take = [&](size_t bytes) { const size_t x = at; at += align256(bytes); return x; };
+    const size_t state = sizeof(float) * (size_t)a.H * a.dk * a.dv;
+    for (int d = 0; d < dirs; ++d) {
+        l.X[d] = take((size_t)l.slots * state);
+        l.seg[d] = take((size_t)l.seg_slots * state);
+        l.keep[d] = take((size_t)l.seg_slots * a.H * sizeof(float));
+    }
+    l.bytes = at;
+    return l;
+}
+
+template <typename Tin, int DK, int DV>
+cudaError_t states(const HlaArgs &a, const Layout &l, int dirs, StateArgs &s) {
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    s.a = a;
+    if (dirs == 2) s.a.ST = nullptr;
+    s.seg.sc = l.sc;
+    for (int d = 0; d < dirs; ++d) {
+        s.X[d] = reinterpret_cast<float *>(ws + l.X[d]);
+        s.seg.state[d] = reinterpret_cast<float *>(ws + l.seg[d]);
+        s.seg.keep[d] = reinterpret_cast<float *>(ws + l.keep[d]);
+    }
+    const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), DV / JB, dirs);
+    cudaError_t e;
+    if (l.sc) {
+        s.ends = true;
+        hla_state_simt_kernel<Tin, DK, DV><<<grid, NT, 0, a.stream>>>(s);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_hla_segment_scan(a, s.seg, l.sc * C, dirs)) != cudaSuccess) return e;
+    }
+    s.ends = false;
+    hla_state_simt_kernel<Tin, DK, DV><<<grid, NT, 0, a.stream>>>(s);
+    return cudaGetLastError();
+}
+
 template <typename Tin, int DK, int DV>
 cudaError_t forward_t(const HlaArgs &a) {
-    float *Sc = static_cast<float *>(a.workspace);
-    const long long slots = hla_slots(a.cu_seqlens != nullptr, a.N, a.T, C);
-    hla_state_simt_kernel<Tin, DK, DV, false><<<dim3((unsigned)(a.N * a.H), DV / JB), NT, 0, a.stream>>>(a, Sc);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || slots == 0 || a.T == 0) return e;
+    const Layout l = layout(a, false);
+    StateArgs s{};
+    cudaError_t e = states<Tin, DK, DV>(a, l, 1, s);
+    if (e != cudaSuccess || l.slots == 0 || a.T == 0) return e;
     const auto kern = hla_out_simt_kernel<Tin, DK, DV>;
     constexpr size_t bytes = OutSmem<DK, DV>::bytes;
     if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
-    kern<<<(unsigned)(slots * a.H), NT, bytes, a.stream>>>(a, Sc);
+    kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.X[0]);
     return cudaGetLastError();
 }
 
 template <typename Tin, int DK, int DV>
 cudaError_t backward_t(const HlaArgs &a) {
-    const long long slots = hla_slots(a.cu_seqlens != nullptr, a.N, a.T, C);
-    float *Sc = static_cast<float *>(a.workspace), *Rc = Sc + (size_t)slots * a.H * DV * DK;
-    const dim3 grid((unsigned)(a.N * a.H), DV / JB);
-    HlaArgs f = a;
-    f.ST = nullptr;
-    hla_state_simt_kernel<Tin, DK, DV, false><<<grid, NT, 0, a.stream>>>(f, Sc);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    hla_state_simt_kernel<Tin, DK, DV, true><<<grid, NT, 0, a.stream>>>(a, Rc);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || slots == 0 || a.T == 0) return e;
+    const Layout l = layout(a, true);
+    StateArgs s{};
+    cudaError_t e = states<Tin, DK, DV>(a, l, 2, s);
+    if (e != cudaSuccess || l.slots == 0 || a.T == 0) return e;
     const auto kern = hla_grad_simt_kernel<Tin, DK, DV>;
     constexpr size_t bytes = GradSmem<DK, DV>::bytes;
     if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
-    kern<<<(unsigned)(slots * a.H), NT, bytes, a.stream>>>(a, Sc, Rc);
+    kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.X[0], s.X[1]);
     return cudaGetLastError();
 }
 
@@ -519,16 +690,26 @@ cudaError_t pass(const HlaArgs &a, bool back) {
 
 }  // namespace
 
-size_t hla_forward_simt_workspace(const HlaArgs &a) {
-    return sizeof(float) * (size_t)hla_slots(a.cu_seqlens != nullptr, a.N, a.T, C) * a.H * a.dk * a.dv;
+int hla_segment_chunks(const HlaArgs &a, int C_, long long chains, long long slots) {
+    const long long chunks = ((long long)a.T + C_ - 1) / C_;  // of the longest sequence, at most
+    const long long parts = slots / chains;                    // of each sequence
+    if (parts < 2) return 0;
+    const long long sc = (chunks + parts - 1) / parts;
+    return 2 * sc + 6 < chunks ? (int)sc : 0;
 }
+
+cudaError_t launch_hla_segment_scan(const HlaArgs &a, const HlaSegments &s, int tokens, int dirs) {
+    hla_segment_scan_kernel<<<dim3((unsigned)(a.N * a.H), (a.dk * a.dv + 1023) / 1024, dirs), 256, 0, a.stream>>>(a, s, tokens);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_hla_clear_outside(const HlaArgs &a) {
     const unsigned grid = (unsigned)(a.T < 1024 ? a.T : 1024);
     if (a.dtype == KDA_DTYPE_BF16) hla_clear_outside_kernel<__nv_bfloat16><<<grid, NT, 0, a.stream>>>(a);
     else hla_clear_outside_kernel<float><<<grid, NT, 0, a.stream>>>(a);
     return cudaGetLastError();
 }
-size_t hla_backward_simt_workspace(const HlaArgs &a) { return 2 * hla_forward_simt_workspace(a); }
+size_t hla_simt_workspace(const HlaArgs &a, bool back) { return layout(a, back).bytes; }
 cudaError_t launch_hla_forward_simt(const HlaArgs &a) { return pass(a, false); }
 cudaError_t launch_hla_backward_simt(const HlaArgs &a) { return pass(a, true); }
 

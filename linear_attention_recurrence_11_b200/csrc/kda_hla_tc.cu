@@ -158,9 +158,7 @@ struct ChainArgs {
     HlaArgs a;
     const uint8_t *gates;
     uint8_t *blob[2];   // kStates, per direction: chunk operands [slot][H]
-    float *seg[2];      // per direction: states of the segments [segment slot][H][dv][dk]
-    float *seg_keep[2]; // per direction: decay over each segment [segment slot][H]
-    int sc;             // chunks per segment; 0: whole sequences
+    HlaSegments seg;
     const int32_t *order;  // packed batches: sequences, longest first (null: as they come)
 };
 
@@ -204,21 +202,20 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const long long su = blockIdx.x / p.H;  // sequence, or segment slot
     int n = (int)su, sg = 0;
     HlaSpan sp;
-    if (s.sc) {
-        hla_chunk_of(p, su, s.sc * C, n, sg, sp);
-        if (sg < 0 || sg >= max(1, sp.nch)) return;  // (an empty sequence keeps one segment, which passes its state on)
+    if (s.seg.sc) {
+        if (!hla_segment_of(p, su, s.seg.sc * C, n, sg)) return;
     } else if (s.order) {
         n = s.order[n];
     }
     sp = hla_span(p, n, C);
-    const int nseg = s.sc ? max(1, (sp.nch + s.sc - 1) / s.sc) : 1;
-    const int c0 = s.sc ? sg * s.sc : 0, c1 = s.sc ? min(sp.nch, c0 + s.sc) : sp.nch, nc = c1 - c0;
+    const int nseg = s.seg.sc ? max(1, (sp.nch + s.seg.sc - 1) / s.seg.sc) : 1;
+    const int c0 = s.seg.sc ? sg * s.seg.sc : 0, c1 = s.seg.sc ? min(sp.nch, c0 + s.seg.sc) : sp.nch, nc = c1 - c0;
     const bool last = dir ? sg == 0 : sg == nseg - 1;  // the segment whose end is the sequence's
     if (kMode == kEnds && last) return;
     const size_t base_n = ((size_t)n * p.H + h) * (size_t)(p.dv * p.dk), base_s = ((size_t)su * p.H + h) * (size_t)(p.dv * p.dk);
-    const float *start = kMode == kEnds ? nullptr : s.sc ? s.seg[dir] + base_s : dir ? p.dST : p.S0;
-    if (start && !s.sc) start += base_n;
-    float *end = kMode == kEnds ? s.seg[dir] + base_s : (!last ? nullptr : dir ? p.dS0 : p.ST);
+    const float *start = kMode == kEnds ? nullptr : s.seg.sc ? s.seg.state[dir] + base_s : dir ? p.dST : p.S0;
+    if (start && !s.seg.sc) start += base_n;
+    float *end = kMode == kEnds ? s.seg.state[dir] + base_s : (!last ? nullptr : dir ? p.dS0 : p.ST);
     if (end && kMode != kEnds) end += base_n;
     const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
     const auto rows_of = [&](int i) { return min(C, sp.len - chunk(i) * C); };
@@ -464,7 +461,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int e = 0; e < NX; e += 4)
                 if (col + e < p.dk) *reinterpret_cast<float4 *>(end + row_off + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         }
-        if (kMode == kEnds && ok && tid == 256) s.seg_keep[dir][su * p.H + h] = total;
+        if (kMode == kEnds && ok && tid == 256) s.seg.keep[dir][su * p.H + h] = total;
         if (kMode != kEnds && lane == 0) bulk_wait_read_all();
     } else {
         regs_dec<64>();
@@ -575,38 +572,6 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, kMode == kOut ? 512 : 128);
-    }
-}
-
-// End states of the segments -> their start states: start_0 = S0, start_{i+1} = keep_i start_i + end_i (in the
-// direction's order), in place, one thread per four elements of a (sequence, head).
-__global__ void __launch_bounds__(256) hla_segment_scan_kernel(const ChainArgs s) {
-    constexpr int U = 8;  // end states on their way at once
-    const HlaArgs &p = s.a;
-    const int dir = blockIdx.z, h = blockIdx.x % p.H, n = blockIdx.x / p.H;
-    const int at = 4 * (blockIdx.y * 256 + threadIdx.x), size = p.dv * p.dk;
-    if (at >= size) return;
-    const HlaSpan sp = hla_span(p, n, s.sc * C);
-    const int nseg = max(1, sp.nch);
-    const float *first = dir ? p.dST : p.S0;
-    float4 x = first ? *reinterpret_cast<const float4 *>(first + ((size_t)n * p.H + h) * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto where = [&](int i) { return (size_t)(sp.slot + (dir ? nseg - 1 - i : i)) * p.H + h; };
-    for (int i0 = 0; i0 < nseg; i0 += U) {
-        float4 e[U];
-        float keep[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (i0 + j + 1 < nseg) {  // (the last segment's end is the sequence's: it has no slot)
-                e[j] = *reinterpret_cast<const float4 *>(s.seg[dir] + where(i0 + j) * size + at);
-                keep[j] = s.seg_keep[dir][where(i0 + j)];
-            }
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-            if (i0 + j < nseg) {
-                *reinterpret_cast<float4 *>(s.seg[dir] + where(i0 + j) * size + at) = x;
-                if (i0 + j + 1 < nseg)
-                    x = make_float4(fmaf(keep[j], x.x, e[j].x), fmaf(keep[j], x.y, e[j].y), fmaf(keep[j], x.z, e[j].z), fmaf(keep[j], x.w, e[j].w));
-            }
     }
 }
 
@@ -1056,18 +1021,6 @@ bool make_tile_map(CUtensorMap *m, const void *base, size_t tokens, int H, int d
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Chunks per segment (0: whole sequences). A chain's chunks run one after another; where there are too few chains to
-// fill the GPU (one CTA per SM), sequences are cut into segments that run side by side, at the price of a pass
-// for their end states, a scan over those, and two launches: as long as half a dozen chunks.
-int segment_chunks(const HlaArgs &a, int dirs) {
-    const long long chains = (long long)a.N * a.H * dirs, sms = device_sm_count();
-    const long long chunks = a.cu_seqlens ? ((long long)a.T + C - 1) / C : ((long long)a.T + C - 1) / C;  // of the longest sequence, at most
-    const long long parts = sms / chains;  // of each sequence
-    if (parts < 2) return 0;
-    const long long sc = (chunks + parts - 1) / parts;
-    return 2 * sc + 6 < chunks ? (int)sc : 0;
-}
-
 struct Layout {
     int sc;
     bool order;
@@ -1078,7 +1031,7 @@ Layout layout(const HlaArgs &a, bool back) {
     Layout l{};
     const int dirs = back ? 2 : 1, dkp = padded(a.dk), dvp = padded(a.dv);
     const bool packed = a.cu_seqlens != nullptr;
-    l.sc = segment_chunks(a, dirs);
+    l.sc = hla_segment_chunks(a, C, (long long)a.N * a.H * dirs, device_sm_count());  // one chain's CTA per SM
     l.slots = hla_slots(packed, a.N, a.T, C);
     l.seg_slots = l.sc ? hla_slots(packed, a.N, a.T, l.sc * C) : 0;
     size_t at = 0;
@@ -1127,12 +1080,12 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     ChainArgs s{};
     s.a = a;
     if (back) s.a.ST = nullptr;
-    s.sc = l.sc;
+    s.seg.sc = l.sc;
     s.gates = ws + l.gates;
     for (int d = 0; d < dirs; ++d) {
         s.blob[d] = ws + l.blob[d];
-        s.seg[d] = reinterpret_cast<float *>(ws + l.seg[d]);
-        s.seg_keep[d] = reinterpret_cast<float *>(ws + l.keep[d]);
+        s.seg.state[d] = reinterpret_cast<float *>(ws + l.seg[d]);
+        s.seg.keep[d] = reinterpret_cast<float *>(ws + l.keep[d]);
     }
     cudaError_t e;
     if (l.order) {
@@ -1145,8 +1098,7 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (l.sc) {
         if ((e = chain<DKP, DVP, kEnds>(s, m, l, dirs)) != cudaSuccess) return e;
-        hla_segment_scan_kernel<<<dim3((unsigned)(a.N * a.H), (a.dk * a.dv + 1023) / 1024, dirs), 256, 0, a.stream>>>(s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_hla_segment_scan(a, s.seg, l.sc * C, dirs)) != cudaSuccess) return e;
     }
     if (!back) return chain<DKP, DVP, kOut>(s, m, l, 1);
     if ((e = chain<DKP, DVP, kStates>(s, m, l, 2)) != cudaSuccess) return e;
