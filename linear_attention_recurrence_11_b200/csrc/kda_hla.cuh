@@ -17,8 +17,8 @@
 //
 // The decays are differences of cumulative sums. The sums are exact (integers of 2^-40) and kept as
 // the sum of two floats, so that a difference of two nearby large values (strong decays earlier in
-// the chunk) keeps its own precision: D_rs = 2^{(hi_r - hi_s) + (lo_r - lo_s)}. A g below -kMaxLog2
-// in units of log2 (-infinity among them) counts as -kMaxLog2: 2^-200 is zero in fp32.
+// the chunk) keeps its own precision: D_rs = 2^{(hi_r - hi_s) + (lo_r - lo_s)}. A g below -kMaxGate
+// (-infinity among them) counts as -kMaxGate: e^-138 is zero in fp32.
 #pragma once
 
 #include "kda_internal.cuh"
@@ -99,8 +99,7 @@ __device__ __forceinline__ bool hla_chunk_of(const HlaArgs &p, long long slot, i
     return c >= 0 && c < s.nch;
 }
 
-constexpr double kLog2eD = 1.4426950408889634;
-constexpr double kMaxLog2 = 200.0;
+constexpr float kMaxGate = 138.f;  // 2^-199 and 2^199
 
 __device__ __forceinline__ float hla_ex2(float x) {
     float y;
@@ -112,7 +111,10 @@ __device__ __forceinline__ float hla_decay(float2 a, float2 b) { return hla_ex2(
 
 // A log-decay in units of log2 as an integer of 2^-40, and a sum of them as two floats.
 __device__ __forceinline__ long long hla_gate_fixed(float g) {
-    return __double2ll_rn(fmin(fmax((double)g * kLog2eD, -kMaxLog2), kMaxLog2) * 1099511627776.0);
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2 e in two floats: the product keeps 48 bits
+    g = fminf(fmaxf(g, -kMaxGate), kMaxGate);
+    const float p = g * kHi, e = fmaf(g, kLo, fmaf(g, kHi, -p));
+    return __float2ll_rn(p * 1099511627776.f) + __float2ll_rn(e * 1099511627776.f);  // 2^40
 }
 __device__ __forceinline__ float2 hla_gate_split(long long t) {
     const float hi = __ll2float_rn(t);                        // 24 bits

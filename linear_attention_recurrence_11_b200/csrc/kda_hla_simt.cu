@@ -1,7 +1,7 @@
 // Linear attention with one decay per head in fp32 accuracy (fp32 or bf16 storage, any of the head sizes):
 // prefill and its backward pass, in chunks of 64 tokens. The chunked form is in kda_hla.cuh.
 //
-// Three kernels. The state kernel walks the chunks of a (sequence, head, 32 rows of dv) in order and writes the
+// Three kernels. The state kernel walks the chunks of a (sequence, head, 64 rows of dv) in order and writes the
 // state before each chunk (or, from the last chunk to the first, the state's gradient behind it); the rows of S^T
 // evolve independently, so the split over dv is exact, and where chains are few the sequences are cut into
 // segments. The output and gradient kernels then take every chunk on its own.
@@ -17,7 +17,7 @@ namespace {
 
 constexpr int C = 64;
 constexpr int NT = 256;
-constexpr int JB = 32;      // dv rows of a state tile
+constexpr int JB = 32;      // dv rows of a state tile of the gradients
 constexpr int LP = C + 4;   // row strides are 4 mod 32 floats: the fragments' reads along rows hit all banks
 
 // ------------------------------------------------------------------ products
@@ -155,15 +155,23 @@ struct StateArgs {
     bool ends;
 };
 
+// One CTA: ROWS rows of dv; its 8 warps 2 x 4 over 64 rows, or 1 x 8 (1 x 4) over 32.
+template <int DK, int DV>
+struct StateTile {
+    static constexpr int ROWS = DV < 64 ? 32 : 64, WN = ROWS == 64 ? 4 : DK < 64 ? 4 : 8, NJ = DK / (8 * WN);
+    static constexpr int KP = DK + 8, VP = ROWS + 8;  // (read down the columns: 8 mod 32)
+    static constexpr size_t bytes = sizeof(float) * C * (KP + VP) + sizeof(float2) * C;
+};
+
 template <typename Tin, int DK, int DV>
 __global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
-    constexpr int KP = DK + 8, VP = JB + 8;  // (read down the columns: 8 mod 32)
-    constexpr int WN = DK < 64 ? 4 : 8, NJ = DK / (8 * WN);
+    using L = StateTile<DK, DV>;
+    constexpr int KP = L::KP, VP = L::VP, WN = L::WN, NJ = L::NJ, ROWS = L::ROWS;
     const HlaArgs &p = s.a;
-    __shared__ __align__(16) float sA[C * KP];
-    __shared__ __align__(16) float sB[C * VP];
-    __shared__ float2 G[C];
-    const int dir = blockIdx.z, j0 = blockIdx.y * JB, h = blockIdx.x % p.H;
+    extern __shared__ __align__(16) float smem[];
+    float *sA = smem, *sB = sA + C * KP;
+    float2 *G = reinterpret_cast<float2 *>(sB + C * VP);
+    const int dir = blockIdx.z, j0 = blockIdx.y * ROWS, h = blockIdx.x % p.H;
     const long long su = blockIdx.x / p.H;
     int n = (int)su, sg = 0;
     HlaSpan sp;
@@ -180,8 +188,8 @@ __global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
     if (end && !s.ends) end += base_n;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const WarpTile w{0, 8 * (warp % WN), lane >> 2, lane & 3};
-    const bool active = warp < WN;
+    const WarpTile w{ROWS == 64 ? 32 * (warp >> 2) : 0, 8 * (warp % WN), lane >> 2, lane & 3};
+    const bool active = ROWS == 64 || warp < WN;
     float x[2][NJ][4];
     const auto each = [&](auto f) {  // (pairs of columns)
         if (active)
@@ -200,7 +208,7 @@ __global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
     });
     const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
     TileRegs<Tin, DK, DK> ta;
-    TileRegs<Tin, DV, JB> tb;
+    TileRegs<Tin, DV, ROWS> tb;
     HlaGate<Tin, C> gate;
     const auto load = [&](int i) {
         const int c = chunk(i), Lc = min(C, sp.len - c * C);
@@ -601,7 +609,7 @@ Layout layout(const HlaArgs &a, bool back) {
     const int dirs = back ? 2 : 1;
     const bool packed = a.cu_seqlens != nullptr;
     // up to four state CTAs run on an SM
-    l.sc = hla_segment_chunks(a, C, (long long)a.N * a.H * (a.dv / JB) * dirs, 4LL * device_sm_count());
+    l.sc = hla_segment_chunks(a, C, (long long)a.N * a.H * ((a.dv + 63) / 64) * dirs, 4LL * device_sm_count());
     l.slots = hla_slots(packed, a.N, a.T, C);
     l.seg_slots = l.sc ? hla_slots(packed, a.N, a.T, l.sc * C) : 0;
     size_t at = 0;
@@ -627,16 +635,19 @@ cudaError_t states(const HlaArgs &a, const Layout &l, int dirs, StateArgs &s) {
         s.seg.state[d] = reinterpret_cast<float *>(ws + l.seg[d]);
         s.seg.keep[d] = reinterpret_cast<float *>(ws + l.keep[d]);
     }
-    const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), DV / JB, dirs);
-    cudaError_t e;
+    using T = StateTile<DK, DV>;
+    const auto kern = hla_state_simt_kernel<Tin, DK, DV>;
+    cudaError_t e = with_smem(kern, T::bytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), DV / T::ROWS, dirs);
     if (l.sc) {
         s.ends = true;
-        hla_state_simt_kernel<Tin, DK, DV><<<grid, NT, 0, a.stream>>>(s);
+        kern<<<grid, NT, T::bytes, a.stream>>>(s);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if ((e = launch_hla_segment_scan(a, s.seg, l.sc * C, dirs)) != cudaSuccess) return e;
     }
     s.ends = false;
-    hla_state_simt_kernel<Tin, DK, DV><<<grid, NT, 0, a.stream>>>(s);
+    kern<<<grid, NT, T::bytes, a.stream>>>(s);
     return cudaGetLastError();
 }
 

@@ -35,6 +35,12 @@ __host__ __device__ inline size_t blob_bytes(int dkp, int dvp) { return (size_t)
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
+// 32 consecutive TMEM columns of this thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+    tmem_ld16(addr, *reinterpret_cast<float(*)[16]>(v));
+    tmem_ld16(addr + 16u, *reinterpret_cast<float(*)[16]>(v + 16));
+}
+
 // =================================================================== gates
 // Of every (chunk slot, head), once for all kernels: the cumulative log2-decays G[128] as two floats each, and the
 // factors F[s] = 2^{G_e - G_s}, e the last of the 32 tokens that s is among (1.5 KB). A block takes 32 heads, whose
@@ -43,17 +49,18 @@ constexpr uint32_t GATE = C * 8 + C * 4;
 
 __global__ void __launch_bounds__(256) hla_gate_kernel(const HlaArgs p, uint8_t *__restrict__ gates) {
     constexpr int E = 16, SEGS = C / E;
+    constexpr int LG = 33;  // row stride: read down the columns
     __shared__ long long tot[SEGS][32];
-    __shared__ float2 ends[SEGS][32];
     __shared__ int nans[SEGS][32];
+    __shared__ float2 sG[C * LG];  // [token][head]
     const long long slot = blockIdx.x;
-    const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5, h = blockIdx.y * 32 + lane;
+    const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5;
     int n, c;
     HlaSpan sp;
     if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
     const int Lc = min(C, sp.len - c * C);
     const size_t row0 = (size_t)(sp.t0 + (long long)c * C);
-    const int hh = min(h, p.H - 1);
+    const int hh = min((int)(blockIdx.y * 32) + lane, p.H - 1);
     float g[E];
     if (p.gate == KDA_HLA_GATE_HEAD) {
         const float x = static_cast<const float *>(p.g)[hh];
@@ -85,24 +92,24 @@ __global__ void __launch_bounds__(256) hla_gate_kernel(const HlaArgs p, uint8_t 
             before += tot[k][lane];
             nan_before |= nans[k][lane] != 0;
         }
-    float2 G[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        G[e] = hla_gate_split(before + x[e]);
-        if (nan_before || e >= first_nan) G[e].x = __int_as_float(0x7fffffff);
+        float2 G = hla_gate_split(before + x[e]);
+        if (nan_before || e >= first_nan) G.x = __int_as_float(0x7fffffff);
+        sG[(seg * E + e) * LG + lane] = G;
     }
-    ends[seg][lane] = G[E - 1];
     __syncthreads();
-    if (h >= p.H) return;
-    const float2 ge = ends[seg | 1][lane];
-    uint8_t *dst = gates + ((size_t)slot * p.H + h) * GATE;
+    // out by heads, a warp each: 256 and 128 contiguous bytes at a time
+    for (int i = seg; i < 32 && blockIdx.y * 32 + i < p.H; i += SEGS) {
+        uint8_t *dst = gates + ((size_t)slot * p.H + blockIdx.y * 32 + i) * GATE;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<float4 *>(dst + (seg * E + e) * 8) = make_float4(G[e].x, G[e].y, G[e + 1].x, G[e + 1].y);
-#pragma unroll
-    for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<float4 *>(dst + C * 8 + (seg * E + e) * 4) =
-            make_float4(hla_decay(ge, G[e]), hla_decay(ge, G[e + 1]), hla_decay(ge, G[e + 2]), hla_decay(ge, G[e + 3]));
+        for (int k = 0; k < C / 32; ++k) {
+            const int s = 32 * k + lane;
+            const float2 G = sG[s * LG + i];
+            *reinterpret_cast<float2 *>(dst + s * 8) = G;
+            *reinterpret_cast<float *>(dst + C * 8 + s * 4) = hla_decay(sG[(32 * k + 31) * LG + i], G);
+        }
+    }
 }
 
 // Masked decayed scores of one TMEM row r (in the 32 rows from R on) and the 32 columns from `col` on, in bf16 pairs:
@@ -428,8 +435,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int k = 0; k < NO / 32; ++k) {
                 const int c = oc + 32 * k;
                 float v[32];
-                tmem_ld16(tmem + tlane + TO + c, *reinterpret_cast<float(*)[16]>(v));
-                tmem_ld16(tmem + tlane + TO + c + 16u, *reinterpret_cast<float(*)[16]>(v + 16));
+                tmem_ld32(tmem + tlane + TO + c, v);
                 tmem_wait_ld();
                 uint4 w[4];
 #pragma unroll
@@ -512,7 +518,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const CUtensorMap *ta = dir ? &tm_q : &tm_k, *tb = dir ? &tm_o : &tm_v;
             int nk = 0, nq = 0, nv = 0;  // loads issued
             for (int i = 0; i < nc && ok; ++i) {
-                const int tok = (int)row_of(i), ahead = i + 2 < nc ? (int)row_of(i + 2) : -1;
+                const int tok = (int)row_of(i);
                 const uint32_t st = NS == 1 ? 0u : (uint32_t)(i & 1);
                 if (kMode == kOut) {
                     if (i > 0) {
@@ -532,7 +538,6 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int b = 0; b < DKP / 64; ++b) {
                     tma_load_3d(sm + L::K + st * L::KT + b * TILE, ta, bars + F_K + st, 64 * b, h, tok);
-                    if (ahead >= 0) tma_prefetch_l2_3d(ta, 64 * b, h, ahead);
                 }
                 if (kMode == kOut) {
                     if (i > 0 && !wait(C_QS, i - 1)) break;
@@ -541,7 +546,6 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                     for (int b = 0; b < DKP / 64; ++b) {
                         tma_load_3d(sm + L::Q + b * TILE, &tm_q, bars + F_Q, 64 * b, h, tok);
-                        if (ahead >= 0) tma_prefetch_l2_3d(&tm_q, 64 * b, h, ahead);
                     }
                     if (i > 0 && !wait(C_PV, i - 1)) break;  // (and the products before it)
                 }
@@ -550,7 +554,6 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int b = 0; b < DVP / 64; ++b) {
                     tma_load_3d(sm + L::V + st * L::VT + b * TILE, tb, bars + F_V + st, 64 * b, h, tok);
-                    if (ahead >= 0) tma_prefetch_l2_3d(tb, 64 * b, h, ahead);
                 }
             }
             // nothing may be in flight when the CTA ends: the last loads into each buffer (bounded)
