@@ -109,83 +109,9 @@ __device__ __forceinline__ float hla_ex2(float x) {
 // 2^(a - b) for sums kept as two floats
 __device__ __forceinline__ float hla_decay(float2 a, float2 b) { return hla_ex2((a.x - b.x) + (a.y - b.y)); }
 
-// A log-decay in units of log2 as an integer of 2^-40, and a sum of them as two floats.
-__device__ __forceinline__ long long hla_gate_fixed(float g) {
-    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2 e in two floats: the product keeps 48 bits
-    g = fminf(fmaxf(g, -kMaxGate), kMaxGate);
-    const float p = g * kHi, e = fmaf(g, kLo, fmaf(g, kHi, -p));
-    return __float2ll_rn(p * 1099511627776.f) + __float2ll_rn(e * 1099511627776.f);  // 2^40
-}
-__device__ __forceinline__ float2 hla_gate_split(long long t) {
-    const float hi = __ll2float_rn(t);                        // 24 bits
-    const float lo = __ll2float_rn(t - __float2ll_rn(hi));    // the rest: a difference of integers
-    return make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);  // 2^-40
-}
-
-// One chunk's log-decays, read by one warp: lane l holds rows l E .. + E - 1 (E = C / 32); rows from Lc on
-// decay by nothing. `row0` is the chunk's first token row. A token's log-decays of all heads are neighbours, a
-// head's are H apart: E loads of 32 sectors each. They are issued together and converted only when they are
-// summed; one at a time, each behind its own bounds check, they took 5 us per chunk.
-template <typename Tin, int C>
-struct HlaGate {
-    Tin raw[C / 32];
-    float head;
-    int Lc;
-    bool by_head;
-
-    __device__ __forceinline__ void load(const HlaArgs &p, long long row0, int h, int Lc_) {
-        Lc = Lc_;
-        by_head = p.gate == KDA_HLA_GATE_HEAD;
-        if (by_head) {
-            head = static_cast<const float *>(p.g)[h];
-        } else {
-#pragma unroll
-            for (int e = 0; e < C / 32; ++e) {
-                const int r = min((int)(threadIdx.x & 31) * (C / 32) + e, Lc - 1);
-                raw[e] = static_cast<const Tin *>(p.g)[(size_t)(row0 + r) * p.H + h];
-            }
-        }
-    }
-    __device__ __forceinline__ float at(int e) const {
-        return (int)(threadIdx.x & 31) * (C / 32) + e >= Lc ? 0.f : by_head ? head : ld_elem(raw, e);
-    }
-};
-// Their cumulative sums G[r] (r < C) in units of log2, as two floats each, by the same warp. The sums are integers
-// of 2^-40: exact, and an addition of two instructions, where fp64 took 1 us per chunk of the chains' time. A NaN
-// makes every sum from its row on one.
-template <typename Tin, int C>
-__device__ __forceinline__ void hla_scan_gate(const HlaGate<Tin, C> &gate, float2 *G) {
-    constexpr int E = C / 32;
-    const int lane = threadIdx.x & 31;
-    long long x[E];
-    int first_nan = E;  // among this lane's rows
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float g = gate.at(e);
-        if (g != g && first_nan == E) first_nan = e;
-        x[e] = hla_gate_fixed(g) + (e ? x[e - 1] : 0);
-    }
-    long long sum = x[E - 1];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += y;
-    }
-    const long long before = sum - x[E - 1];
-    const bool nan_before = (__ballot_sync(0xffffffffu, first_nan < E) & ((1u << lane) - 1u)) != 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        float2 t = hla_gate_split(before + x[e]);
-        if (nan_before || e >= first_nan) t.x = __int_as_float(0x7fffffff);
-        G[lane * E + e] = t;
-    }
-}
-template <typename Tin, int C>
-__device__ __forceinline__ void hla_load_scan_gate(const HlaArgs &p, long long row0, int h, int Lc, float2 *G) {
-    HlaGate<Tin, C> gate;
-    gate.load(p, row0, h, Lc);
-    hla_scan_gate(gate, G);
-}
+// Bytes of a chunk's gates (kda_hla_gate.cuh): G as C times two floats, and C factors.
+template <int C>
+constexpr uint32_t kHlaGateBytes = C * 12;
 
 // Segments. A chain's chunks run one after another; where there are too few chains to fill the GPU, sequences are
 // cut into segments that run side by side, at the price of a pass for their end states, a scan over those, and two

@@ -11,6 +11,7 @@
 // fp32's own rounding. Measured against FFMA register tiles (4 x 8 per thread), the gradients of 16 heads x 2099
 // tokens take 0.4 of the time: a fragment's element is read from shared memory once for 8 to 32 products.
 #include "kda_hla.cuh"
+#include "kda_hla_gate.cuh"
 
 namespace kda {
 namespace {
@@ -18,6 +19,7 @@ namespace {
 constexpr int C = 64;
 constexpr int NT = 256;
 constexpr int JB = 32;      // dv rows of a state tile of the gradients
+constexpr uint32_t GATE = kHlaGateBytes<C>;
 constexpr int LP = C + 4;   // row strides are 4 mod 32 floats: the fragments' reads along rows hit all banks
 
 // ------------------------------------------------------------------ products
@@ -99,6 +101,11 @@ __device__ __forceinline__ void zero(float (&c)[2][NJ][4]) {
             for (int e = 0; e < 4; ++e) c[i][j][e] = 0.f;
 }
 
+// this thread's G of a chunk (threads 0 .. C - 1)
+__device__ __forceinline__ float2 gate_of(const uint8_t *gates, long long slot, int H, int h) {
+    return __ldg(reinterpret_cast<const float2 *>(gates + ((size_t)slot * H + h) * GATE) + threadIdx.x);
+}
+
 // four consecutive elements (8- or 16-byte aligned)
 __device__ __forceinline__ float4 ld4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
 __device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
@@ -150,6 +157,7 @@ __device__ __forceinline__ void load_tile(float *s, int lds, const void *src, lo
 // writes each segment's end state from zero, and the second starts from the segments' start states.
 struct StateArgs {
     HlaArgs a;
+    const uint8_t *gates;
     float *X[2];
     HlaSegments seg;
     bool ends;
@@ -209,11 +217,11 @@ __global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
     const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
     TileRegs<Tin, DK, DK> ta;
     TileRegs<Tin, DV, ROWS> tb;
-    HlaGate<Tin, C> gate;
+    float2 gate;
     const auto load = [&](int i) {
         const int c = chunk(i), Lc = min(C, sp.len - c * C);
         const long long row0 = sp.t0 + (long long)c * C;
-        if (warp == 0) gate.load(p, row0, h, Lc);
+        if (threadIdx.x < C) gate = gate_of(s.gates, sp.slot + c, p.H, h);
         ta.load(dir ? p.q : p.k, row0, p.H, h, 0, Lc);
         tb.load(dir ? p.dO : p.v, row0, p.H, h, j0, Lc);
     };
@@ -224,7 +232,7 @@ __global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
             float *dst = s.X[dir] + ((size_t)(sp.slot + chunk(i)) * p.H + h) * (size_t)(DV * DK);
             each([&](size_t at, float &u, float &v) { *reinterpret_cast<float2 *>(dst + at) = make_float2(u, v); });
         }
-        if (warp == 0) hla_scan_gate(gate, G);
+        if (threadIdx.x < C) G[threadIdx.x] = gate;
         ta.store(sA, KP, [&](int) { return 1.f; });
         __syncthreads();
         const float2 g0 = make_float2(0.f, 0.f), gC = G[C - 1];
@@ -289,7 +297,7 @@ struct OutSmem {
 };
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const float *__restrict__ Sc) {
+__global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const uint8_t *__restrict__ gates, const float *__restrict__ Sc) {
     using L = OutSmem<DK, DV>;
     constexpr int VJ = DV / 32;
     extern __shared__ __align__(16) float smem[];
@@ -308,7 +316,7 @@ __global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const
     load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc, p.scale);
     load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
-    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
+    if (threadIdx.x < C) G[threadIdx.x] = gate_of(gates, slot, p.H, h);
     __syncthreads();
     {
         float a[2][2][4];
@@ -386,7 +394,7 @@ struct GradSmem {
 };
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, const float *__restrict__ Sc,
+__global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, const uint8_t *__restrict__ gates, const float *__restrict__ Sc,
                                                            const float *__restrict__ Rc) {
     using L = GradSmem<DK, DV>;
     constexpr int KJ = DK / 32, VJ = DV / 32;
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
     load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
     load_tile<Tin, DV, DV>(sO, L::VP, p.dO, row0, p.H, h, 0, Lc, p.scale);
-    if (threadIdx.x < 32) hla_load_scan_gate<Tin, C>(p, row0, h, Lc, G);
+    if (threadIdx.x < C) G[threadIdx.x] = gate_of(gates, slot, p.H, h);
     __syncthreads();
 
     // the parts that go through the states: dQ from S_in, dK and dV from R, and their terms of dg
@@ -602,7 +610,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 struct Layout {
     int sc;
     long long slots, seg_slots;
-    size_t X[2], seg[2], keep[2], bytes;
+    size_t gates, X[2], seg[2], keep[2], bytes;
 };
 Layout layout(const HlaArgs &a, bool back) {
     Layout l{};
@@ -615,6 +623,7 @@ Layout layout(const HlaArgs &a, bool back) {
     size_t at = 0;
     const auto take = [&](size_t bytes) { const size_t x = at; at += align256(bytes); return x; };
     const size_t state = sizeof(float) * (size_t)a.H * a.dk * a.dv;
+    l.gates = take((size_t)l.slots * a.H * GATE);
     for (int d = 0; d < dirs; ++d) {
         l.X[d] = take((size_t)l.slots * state);
         l.seg[d] = take((size_t)l.seg_slots * state);
@@ -630,6 +639,7 @@ cudaError_t states(const HlaArgs &a, const Layout &l, int dirs, StateArgs &s) {
     s.a = a;
     if (dirs == 2) s.a.ST = nullptr;
     s.seg.sc = l.sc;
+    s.gates = ws + l.gates;
     for (int d = 0; d < dirs; ++d) {
         s.X[d] = reinterpret_cast<float *>(ws + l.X[d]);
         s.seg.state[d] = reinterpret_cast<float *>(ws + l.seg[d]);
@@ -639,6 +649,7 @@ cudaError_t states(const HlaArgs &a, const Layout &l, int dirs, StateArgs &s) {
     const auto kern = hla_state_simt_kernel<Tin, DK, DV>;
     cudaError_t e = with_smem(kern, T::bytes);
     if (e != cudaSuccess) return e;
+    if (l.slots > 0 && (e = launch_hla_gates<Tin, C>(a, l.slots, ws + l.gates)) != cudaSuccess) return e;
     const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), DV / T::ROWS, dirs);
     if (l.sc) {
         s.ends = true;
@@ -660,7 +671,7 @@ cudaError_t forward_t(const HlaArgs &a) {
     const auto kern = hla_out_simt_kernel<Tin, DK, DV>;
     constexpr size_t bytes = OutSmem<DK, DV>::bytes;
     if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
-    kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.X[0]);
+    kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.gates, s.X[0]);
     return cudaGetLastError();
 }
 
@@ -673,7 +684,7 @@ cudaError_t backward_t(const HlaArgs &a) {
     const auto kern = hla_grad_simt_kernel<Tin, DK, DV>;
     constexpr size_t bytes = GradSmem<DK, DV>::bytes;
     if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
-    kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.X[0], s.X[1]);
+    kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.gates, s.X[0], s.X[1]);
     return cudaGetLastError();
 }
 

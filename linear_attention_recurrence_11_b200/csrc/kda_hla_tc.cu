@@ -11,6 +11,7 @@
 // decay per token; that product is taken as the sum of two bf16 numbers (hi + lo, 16 bits of the 24),
 // so that the fp32 state is good to about 2^-18 and not to 2^-9.
 #include "kda_hla.cuh"
+#include "kda_hla_gate.cuh"
 #include "kda_sm100.cuh"
 #include "kda_tc_common.cuh"
 
@@ -41,76 +42,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
     tmem_ld16(addr + 16u, *reinterpret_cast<float(*)[16]>(v + 16));
 }
 
-// =================================================================== gates
-// Of every (chunk slot, head), once for all kernels: the cumulative log2-decays G[128] as two floats each, and the
-// factors F[s] = 2^{G_e - G_s}, e the last of the 32 tokens that s is among (1.5 KB). A block takes 32 heads, whose
-// log-decays of a token are neighbours, and 16 tokens per thread.
-constexpr uint32_t GATE = C * 8 + C * 4;
-
-__global__ void __launch_bounds__(256) hla_gate_kernel(const HlaArgs p, uint8_t *__restrict__ gates) {
-    constexpr int E = 16, SEGS = C / E;
-    constexpr int LG = 33;  // row stride: read down the columns
-    __shared__ long long tot[SEGS][32];
-    __shared__ int nans[SEGS][32];
-    __shared__ float2 sG[C * LG];  // [token][head]
-    const long long slot = blockIdx.x;
-    const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5;
-    int n, c;
-    HlaSpan sp;
-    if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
-    const int Lc = min(C, sp.len - c * C);
-    const size_t row0 = (size_t)(sp.t0 + (long long)c * C);
-    const int hh = min((int)(blockIdx.y * 32) + lane, p.H - 1);
-    float g[E];
-    if (p.gate == KDA_HLA_GATE_HEAD) {
-        const float x = static_cast<const float *>(p.g)[hh];
-#pragma unroll
-        for (int e = 0; e < E; ++e) g[e] = x;
-    } else {
-        __nv_bfloat16 raw[E];  // (read together: one wait for all)
-#pragma unroll
-        for (int e = 0; e < E; ++e) raw[e] = static_cast<const __nv_bfloat16 *>(p.g)[(row0 + min(seg * E + e, Lc - 1)) * p.H + hh];
-#pragma unroll
-        for (int e = 0; e < E; ++e) g[e] = __bfloat162float(raw[e]);
-    }
-    long long x[E];
-    int first_nan = E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float v = seg * E + e < Lc ? g[e] : 0.f;
-        if (v != v && first_nan == E) first_nan = e;
-        x[e] = hla_gate_fixed(v) + (e ? x[e - 1] : 0);
-    }
-    tot[seg][lane] = x[E - 1];
-    nans[seg][lane] = first_nan < E;
-    __syncthreads();
-    long long before = 0;
-    bool nan_before = false;
-#pragma unroll
-    for (int k = 0; k < SEGS; ++k)
-        if (k < seg) {
-            before += tot[k][lane];
-            nan_before |= nans[k][lane] != 0;
-        }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        float2 G = hla_gate_split(before + x[e]);
-        if (nan_before || e >= first_nan) G.x = __int_as_float(0x7fffffff);
-        sG[(seg * E + e) * LG + lane] = G;
-    }
-    __syncthreads();
-    // out by heads, a warp each: 256 and 128 contiguous bytes at a time
-    for (int i = seg; i < 32 && blockIdx.y * 32 + i < p.H; i += SEGS) {
-        uint8_t *dst = gates + ((size_t)slot * p.H + blockIdx.y * 32 + i) * GATE;
-#pragma unroll
-        for (int k = 0; k < C / 32; ++k) {
-            const int s = 32 * k + lane;
-            const float2 G = sG[s * LG + i];
-            *reinterpret_cast<float2 *>(dst + s * 8) = G;
-            *reinterpret_cast<float *>(dst + C * 8 + s * 4) = hla_decay(sG[(32 * k + 31) * LG + i], G);
-        }
-    }
-}
+constexpr uint32_t GATE = kHlaGateBytes<C>;
 
 // Masked decayed scores of one TMEM row r (in the 32 rows from R on) and the 32 columns from `col` on, in bf16 pairs:
 // x D_rs, D_rs = 2^{G_r - G_s} for s <= r, and 0 above. Columns that all come before these rows take D_rs as
@@ -1097,8 +1029,7 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
         s.order = order;
     }
     const unsigned units = (unsigned)(l.slots * a.H);
-    hla_gate_kernel<<<dim3((unsigned)l.slots, (a.H + 31) / 32), 256, 0, a.stream>>>(a, ws + l.gates);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_hla_gates<__nv_bfloat16, C>(a, l.slots, ws + l.gates)) != cudaSuccess) return e;
     if (l.sc) {
         if ((e = chain<DKP, DVP, kEnds>(s, m, l, dirs)) != cudaSuccess) return e;
         if ((e = launch_hla_segment_scan(a, s.seg, l.sc * C, dirs)) != cudaSuccess) return e;
