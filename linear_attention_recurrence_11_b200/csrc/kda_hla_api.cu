@@ -24,6 +24,7 @@ int check_sizes(int B, int T, int H, int dk, int dv, int dtype, bool packed, int
     a->N = packed ? num_seqs : B;
     // one block per (sequence, head) and per (chunk slot, head), in 31-bit grids
     if ((long long)a->N * H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if ((long long)B * T > 0x7fffffffLL - 256) return KDA_ERR_UNSUPPORTED;  // tokens are 32-bit coordinates of the copies
     if (kda::hla_slots(packed, a->N, T, 64) > 0x7fffffffLL / H) return KDA_ERR_UNSUPPORTED;
     a->cu_seqlens = packed ? &kPackedMarker : nullptr;
     if (path == KDA_PATH_TC && !kda::hla_tc_supported(*a)) return KDA_ERR_UNSUPPORTED;

@@ -33,7 +33,7 @@ def test_prefill_refusals(K, name, args):
     for bad in (dict(B=0), dict(T=-1), dict(H=0), dict(dtype=2), dict(gate=2), dict(path=3), dict(path=9),
                 dict(cu=FAKE, num_seqs=0), dict(cu=FAKE, num_seqs=2, B=2), dict(q=None), dict(k=None), dict(v=None), dict(g=None)):
         assert f(**bad) == K.KDA_ERR_INVALID_ARG, bad
-    for bad in (dict(dk=48), dict(dv=256), dict(H=1 << 30, B=4), dict(path=2, dtype=0)):
+    for bad in (dict(dk=48), dict(dv=256), dict(H=1 << 30, B=4), dict(path=2, dtype=0), dict(B=1 << 15, T=1 << 16)):
         assert f(**bad) == K.KDA_ERR_UNSUPPORTED, bad
     for n in ("q", "k", "v", "g", "S0", "ws", "status"):
         assert f(**{n: FAKE + 8}) == K.KDA_ERR_ALIGNMENT, n

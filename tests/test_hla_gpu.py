@@ -309,6 +309,41 @@ def test_offsets_past_the_tensors_are_clamped(K):
         torch.cuda.synchronize()
 
 
+def test_more_elements_than_32_bits_count(K):
+    """Tensors and states of more than 2^31 elements: the last tokens, and the last requests, against calls on them alone."""
+    T, H, d, tail = 175000, 96, 128, 300
+    assert T * H * d > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    q, k, v, do = (torch.randn(1, T, H, d, generator=gen, device="cuda", dtype=torch.bfloat16) * 0.1 for _ in range(4))
+    g = -torch.rand(1, T, H, generator=gen, device="cuda").bfloat16() * 0.1
+    end = lambda x: x[:, T - tail:].contiguous()  # noqa: E731
+    _, S0 = K.kda_hla_forward(*(x[:, :T - tail] for x in (q, k, v, g)))
+    o, S = K.kda_hla_forward(q, k, v, g)
+    o2, S2 = K.kda_hla_forward(end(q), end(k), end(v), end(g), S0)
+    assert rel(end(o), o2) < 3 * 2.0 ** -8 and rel(S, S2) < 4 * TOL_STATE["bf16"]
+    del o
+    whole = K.kda_hla_backward(q, k, v, g, do)
+    part = K.kda_hla_backward(*(end(x) for x in (q, k, v, g, do)), S0)
+    for a, b in zip(whole[:4], part[:4]):  # (chunks end elsewhere: other roundings on both sides)
+        assert rel(end(a), b) < 2 * TOL["bf16"]
+    del whole
+    inv, _ = K.kda_rope_inv_freq(64, device="cuda")
+    at = torch.arange(T, device="cuda", dtype=torch.int32).unsqueeze(0)
+    a, _ = K.kda_rope(q, None, inv, positions=at)
+    b, _ = K.kda_rope(end(q), None, inv, positions=at[:, T - tail:].contiguous())
+    assert torch.equal(end(a), b)
+    del q, k, v, do, a
+    N = 1400
+    assert N * H * d * d > 2 ** 31
+    S = torch.randn(N, H, d, d, generator=gen, device="cuda")
+    x = [torch.randn(N, H, d, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(3)]
+    g = -torch.rand(N, H, generator=gen, device="cuda").bfloat16()
+    S2 = S[-2:].clone()
+    o = K.kda_hla_decode_step(*x, g, S)
+    o2 = K.kda_hla_decode_step(*(y[-2:].contiguous() for y in x), g[-2:].contiguous(), S2)
+    assert torch.equal(o[-2:], o2) and torch.equal(S[-2:], S2)
+
+
 def test_python_refusals(K):
     x = inputs(1, 64, 2, 64, 64, "f32", seed=23)
     call = lambda **kw: K.kda_hla_forward(**{**dict(q=x["q"], k=x["k"], v=x["v"], g=x["g"], S0=x["S0"]), **kw})  # noqa: E731

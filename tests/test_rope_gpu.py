@@ -50,6 +50,10 @@ CASES = [  # B, T, Hq, Hk, d, rot, dtype
     (2, 9, 2, 2, 256, 250, "f32"),
     (1, 1025, 8, 1, 64, 64, "f32"),
     (1, 5, 2, 2, 1024, 1024, "bf16"),
+    (1, 3, 70, 70, 1024, 1022, "f32"),
+    (1, 1, 300, 9, 4, 2, "bf16"),
+    (5, 1, 33, 0, 128, 86, "bf16"),
+    (1, 4097, 3, 3, 100, 98, "f32"),
 ]
 
 
@@ -58,7 +62,7 @@ CASES = [  # B, T, Hq, Hk, d, rot, dtype
 def test_rope(K, B, T, Hq, Hk, d, rot, dtype, interleaved):
     gen = torch.Generator(device="cuda").manual_seed(31 + T + rot)
     q = torch.randn(B, T, Hq, d, generator=gen, device="cuda").to(DT[dtype])
-    k = torch.randn(B, T, Hk, d, generator=gen, device="cuda").to(DT[dtype])
+    k = torch.randn(B, T, Hk, d, generator=gen, device="cuda").to(DT[dtype]) if Hk else None
     inv, _ = K.kda_rope_inv_freq(rot, device="cuda")
     pos = torch.randint(0, 5000, (B, T), generator=gen, device="cuda")
     for inverse in (False, True):
@@ -66,7 +70,8 @@ def test_rope(K, B, T, Hq, Hk, d, rot, dtype, interleaved):
             qo, ko = K.kda_rope(q, k, inv, positions=p, interleaved=interleaved, mscale=1.3, inverse=inverse)
             at = torch.arange(T, device="cuda").expand(B, T) if p is None else pos
             check(qo, q, inv, at, interleaved, inverse, 1.3, dtype)
-            check(ko, k, inv, at, interleaved, inverse, 1.3, dtype)
+            if Hk:
+                check(ko, k, inv, at, interleaved, inverse, 1.3, dtype)
 
 
 @pytest.mark.parametrize("at", [0, 1 << 20, (1 << 31) - 5, -3, 1 << 40])
@@ -82,10 +87,11 @@ def test_far_positions(K, at):
     assert ((out.double() - y).abs() <= tol * size).all()
 
 
-def test_in_place_and_q_alone(K):
+@pytest.mark.parametrize("rot", [128, 96, 88, 86, 2])
+def test_in_place_and_q_alone(K, rot):
     q = torch.randn(2, 40, 3, 128, generator=torch.Generator(device="cuda").manual_seed(42), device="cuda").bfloat16()
     k = torch.randn(2, 40, 1, 128, generator=torch.Generator(device="cuda").manual_seed(43), device="cuda").bfloat16()
-    inv, _ = K.kda_rope_inv_freq(96, device="cuda")
+    inv, _ = K.kda_rope_inv_freq(rot, device="cuda")
     for inter in (False, True):
         want = K.kda_rope(q, k, inv, interleaved=inter)
         alone, _ = K.kda_rope(q, None, inv, interleaved=inter)
