@@ -21,9 +21,27 @@
 // (-infinity among them) counts as -kMaxGate: e^-138 is zero in fp32.
 #pragma once
 
+#include <atomic>
+
 #include "kda_internal.cuh"
 
 namespace kda {
+
+// A kernel's dynamic shared memory, raised once per device (one static object per kernel).
+struct HlaSmem {
+    std::atomic<unsigned long long> done{0};
+    template <typename F>
+    cudaError_t raise(F kern, size_t bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 struct HlaArgs {
     const void *q = nullptr, *k = nullptr, *v = nullptr, *g = nullptr;

@@ -599,11 +599,6 @@ __global__ void __launch_bounds__(NT) hla_clear_outside_kernel(const HlaArgs p) 
 }
 
 // ----------------------------------------------------------------- launches
-template <typename F>
-cudaError_t with_smem(F kern, size_t bytes) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace: per direction the states at the chunks' borders, and, with segments, the segments' states and decays.
@@ -647,7 +642,8 @@ cudaError_t states(const HlaArgs &a, const Layout &l, int dirs, StateArgs &s) {
     }
     using T = StateTile<DK, DV>;
     const auto kern = hla_state_simt_kernel<Tin, DK, DV>;
-    cudaError_t e = with_smem(kern, T::bytes);
+    static HlaSmem smem;
+    cudaError_t e = smem.raise(kern, T::bytes);
     if (e != cudaSuccess) return e;
     if (l.slots > 0 && (e = launch_hla_gates<Tin, C>(a, l.slots, ws + l.gates)) != cudaSuccess) return e;
     const dim3 grid((unsigned)((l.sc ? l.seg_slots : a.N) * a.H), DV / T::ROWS, dirs);
@@ -670,7 +666,8 @@ cudaError_t forward_t(const HlaArgs &a) {
     if (e != cudaSuccess || l.slots == 0 || a.T == 0) return e;
     const auto kern = hla_out_simt_kernel<Tin, DK, DV>;
     constexpr size_t bytes = OutSmem<DK, DV>::bytes;
-    if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
+    static HlaSmem smem;
+    if ((e = smem.raise(kern, bytes)) != cudaSuccess) return e;
     kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.gates, s.X[0]);
     return cudaGetLastError();
 }
@@ -683,7 +680,8 @@ cudaError_t backward_t(const HlaArgs &a) {
     if (e != cudaSuccess || l.slots == 0 || a.T == 0) return e;
     const auto kern = hla_grad_simt_kernel<Tin, DK, DV>;
     constexpr size_t bytes = GradSmem<DK, DV>::bytes;
-    if ((e = with_smem(kern, bytes)) != cudaSuccess) return e;
+    static HlaSmem smem;
+    if ((e = smem.raise(kern, bytes)) != cudaSuccess) return e;
     kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.gates, s.X[0], s.X[1]);
     return cudaGetLastError();
 }

@@ -992,7 +992,8 @@ template <int DKP, int DVP, int kMode>
 cudaError_t chain(const ChainArgs &s, const Maps &m, const Layout &l, int dirs) {
     const auto kern = hla_chain_tc_kernel<DKP, DVP, kMode>;
     constexpr size_t bytes = ChainSmem<DKP, DVP, kMode>::bytes;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static HlaSmem smem;
+    const cudaError_t e = smem.raise(kern, bytes);
     if (e != cudaSuccess) return e;
     kern<<<dim3((unsigned)((l.sc ? l.seg_slots : s.a.N) * s.a.H), 1, dirs), kChainThreads, bytes, s.a.stream>>>(m.k, m.v, m.q, m.o, s);
     return cudaGetLastError();
@@ -1044,7 +1045,8 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     t.tiles = units;
     const auto kern = hla_grad_tc_kernel<DKP, DVP>;
     constexpr size_t bytes = GradTile<DKP, DVP>::bytes;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) != cudaSuccess) return e;
+    static HlaSmem smem;
+    if ((e = smem.raise(kern, bytes)) != cudaSuccess) return e;
     const unsigned sms = (unsigned)device_sm_count();
     kern<<<units < sms ? units : sms, 512, bytes, a.stream>>>(m.q, m.k, m.v, m.o, m.dq, m.dk, m.dv, t);
     return cudaGetLastError();

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -578,6 +579,7 @@ def kda_kcp_scan(S0, M, Z, *, stream=None):
 
 # The single-token calls take the GPU two to four microseconds, so what they spend here counts: one test per tensor
 # (_need only says what is wrong with it), no context manager on the current device, plain integers as pointers.
+_NO_SIZE = ctypes.c_size_t(-1).value
 _NO_CONTEXT = contextlib.nullcontext()
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -642,13 +644,22 @@ def _hla_shapes(q, k, v, g, cu_seqlens):
     return dtype, dev, B, T, H, dk, dv, gate, N
 
 
+# (the sizes' own call into the library, for sizes seen before)
+_hla_forward_size = functools.lru_cache(maxsize=4096)(_lib.kda_hla_forward_workspace_size)
+_hla_backward_size = functools.lru_cache(maxsize=4096)(_lib.kda_hla_backward_workspace_size)
+
+
 def _hla_workspace(size, workspace, dev, where):
-    if size == ctypes.c_size_t(-1).value:
+    """Address and bytes of the workspace, and what keeps it alive."""
+    if size == _NO_SIZE:
         raise KdaError(KDA_ERR_UNSUPPORTED, where)
     if workspace is None:
-        return torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        if not size:
+            return None, 0, None
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), size, workspace
     _need(workspace, "workspace", None, None, dev)
-    return workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def kda_hla_forward_workspace_size(B, T, H, dk, dv, num_seqs, dtype, path="auto") -> int:
@@ -676,24 +687,24 @@ def kda_hla_forward(q, k, v, g, S0=None, *, scale: float = 1.0, cu_seqlens=None,
     dtype, dev, B, T, H, dk, dv, gate, N = _hla_shapes(q, k, v, g, cu_seqlens)
     if S0 is not None:
         _check(S0, "S0", torch.float32, (N, H, dv, dk), dev)
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, None, dev)
+    packed = N if cu_seqlens is not None else 0
+    dt, way = DTYPES[dtype], PATHS[path]
+    size = _hla_forward_size(B, T, H, dk, dv, packed, dt, way)
     with _on(dev, stream):
-        if o is None:
-            # tokens outside the sequences of a packed batch are not written
-            o = torch.empty((B, T, H, dv), dtype=dtype, device=dev)
-        _check(o, "o", dtype, (B, T, H, dv), dev)
-        if return_state and S_T is None:
-            S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        if o is None:  # (tokens outside the sequences of a packed batch are not written)
+            o = torch.empty_like(v)
+        else:
+            _check(o, "o", dtype, (B, T, H, dv), dev)
         if S_T is not None:
             _check(S_T, "S_T", torch.float32, (N, H, dv, dk), dev)
-        if dev_status is not None:
-            _need(dev_status, "dev_status", torch.int32, None, dev)
-        packed = N if cu_seqlens is not None else 0
-        size = _lib.kda_hla_forward_workspace_size(B, T, H, dk, dv, packed, DTYPES[dtype], PATHS[path])
-        workspace = _hla_workspace(size, workspace, dev, "kda_hla_forward")
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        rc = _lib.kda_hla_forward(_addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(o), _addr(S_T), B, T, H, dk, dv,
-                                  float(scale), DTYPES[dtype], gate, _addr(cu_seqlens), packed, _addr(workspace), ws_bytes,
-                                  _addr(dev_status), _raw_stream(stream, dev), PATHS[path])
+        elif return_state:
+            S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+        ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_forward")
+        rc = _lib.kda_hla_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), o.data_ptr(), _addr(S_T),
+                                  B, T, H, dk, dv, scale, dt, gate, _addr(cu_seqlens), packed, ws, ws_bytes,
+                                  _addr(dev_status), _raw_stream(stream, dev), way)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_hla_forward")
     return o, S_T
@@ -712,18 +723,18 @@ def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, 
             _check(x, name, torch.float32, (N, H, dv, dk), dev)
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32, None, dev)
+    packed = N if cu_seqlens is not None else 0
+    dt, way = DTYPES[dtype], PATHS[path]
+    size = _hla_backward_size(B, T, H, dk, dv, packed, dt, way)
     with _on(dev, stream):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         dg = torch.empty_like(g) if gate == KDA_HLA_GATE_TOKEN and return_dg else None
         dS0 = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev) if return_dS0 else None
-        packed = N if cu_seqlens is not None else 0
-        size = _lib.kda_hla_backward_workspace_size(B, T, H, dk, dv, packed, DTYPES[dtype], PATHS[path])
-        workspace = _hla_workspace(size, workspace, dev, "kda_hla_backward")
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        rc = _lib.kda_hla_backward(_addr(q), _addr(k), _addr(v), _addr(g), _addr(S0), _addr(do), _addr(dS_T), _addr(dq), _addr(dk_),
-                                   _addr(dv_), _addr(dg), _addr(dS0), B, T, H, dk, dv, float(scale), DTYPES[dtype], gate,
-                                   _addr(cu_seqlens), packed, _addr(workspace), ws_bytes, _addr(dev_status),
-                                   _raw_stream(stream, dev), PATHS[path])
+        ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_backward")
+        rc = _lib.kda_hla_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), do.data_ptr(), _addr(dS_T),
+                                   dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), _addr(dg), _addr(dS0), B, T, H, dk, dv,
+                                   scale, dt, gate, _addr(cu_seqlens), packed, ws, ws_bytes, _addr(dev_status),
+                                   _raw_stream(stream, dev), way)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_hla_backward")
     return dq, dk_, dv_, dg, dS0
@@ -740,11 +751,11 @@ def kda_hla_decode_step(q, k, v, g, S, o=None, *, scale: float = 1.0, stream=Non
     _check(S, "S", torch.float32, (N, H, dv, dk), dev)
     with _on(dev, stream):
         if o is None:
-            o = torch.empty((N, H, dv), dtype=dtype, device=dev)
+            o = torch.empty_like(v)
         else:
             _check(o, "o", dtype, (N, H, dv), dev)
-        rc = _lib.kda_hla_decode_step(_addr(q), _addr(k), _addr(v), _addr(g), _addr(S), _addr(o), N, H, dk, dv, float(scale),
-                                      DTYPES[dtype], gate, _raw_stream(stream, dev))
+        rc = _lib.kda_hla_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), S.data_ptr(), o.data_ptr(), N, H, dk, dv,
+                                      scale, DTYPES[dtype], gate, _raw_stream(stream, dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_hla_decode_step")
     return o
@@ -828,9 +839,9 @@ def kda_rope(q, k, inv_freq, *, positions=None, interleaved: bool = False, mscal
                 k_out = torch.empty_like(k)
             else:
                 _check(k_out, "k_out", dtype, k.shape, dev)
-        rc = _lib.kda_rope(_addr(q), _addr(k), _addr(positions), int(positions is not None and positions.dtype == torch.int64),
-                           _addr(inv_freq), _addr(q_out), _addr(k_out), B, T, Hq, Hk, d, 2 * inv_freq.numel(),
-                           int(interleaved), int(inverse), float(mscale), DTYPES[dtype], _raw_stream(stream, dev))
+        rc = _lib.kda_rope(q.data_ptr(), _addr(k), _addr(positions), int(positions is not None and positions.dtype == torch.int64),
+                           inv_freq.data_ptr(), q_out.data_ptr(), _addr(k_out), B, T, Hq, Hk, d, 2 * inv_freq.numel(),
+                           int(interleaved), int(inverse), mscale, DTYPES[dtype], _raw_stream(stream, dev))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_rope")
     return q_out, k_out
