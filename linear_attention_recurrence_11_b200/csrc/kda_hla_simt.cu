@@ -18,6 +18,7 @@ namespace {
 
 constexpr int C = 64;
 constexpr int NT = 256;
+constexpr int NG = 512;     // of the gradients: one CTA per SM, 4 x 4 warps
 constexpr int JB = 32;      // dv rows of a state tile of the gradients
 constexpr uint32_t GATE = kHlaGateBytes<C>;
 constexpr int LP = C + 4;   // row strides are 4 mod 32 floats: the fragments' reads along rows hit all banks
@@ -33,7 +34,7 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// A warp's part of a product: 32 rows from m0 on, and of every `step` columns 8 from n0 on. With g = lane / 4 and
+// A warp's part of a product: 16 or 32 rows from m0 on, and of every `step` columns 8 from n0 on. With g = lane / 4 and
 // t = lane % 4, c[i][j] holds rows m0 + 16 i + g (elements 0, 1) and + 8 (2, 3), columns n0 + step j + 2 t and + 1.
 struct WarpTile {
     int m0, n0, g, t;
@@ -41,26 +42,27 @@ struct WarpTile {
     template <int kStep>
     __device__ __forceinline__ int col(int j, int e) const { return n0 + kStep * j + 2 * t + (e & 1); }
 };
-// the 8 warps over 64 rows: 2 x 4, and columns in steps of 32
-__device__ __forceinline__ WarpTile tile_2x4() {
+// over 64 rows, and columns in steps of 32: 2 x 4 warps of 32 rows, or 4 x 4 of 16
+template <int kRows>
+__device__ __forceinline__ WarpTile tile_of_warp() {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    return {32 * (warp >> 2), 8 * (warp & 3), lane >> 2, lane & 3};
+    return {kRows * (warp >> 2), 8 * (warp & 3), lane >> 2, lane & 3};
 }
 
 // c += A B over K. A is [m][k], or with kAT [k][m]; B is [k][n], or with kBT [n][k]. The matrix instructions cut their
 // sums off instead of rounding them: over K = 128 that alone came to 3e-6 of the result. So 16 of K at a time are summed
 // by them, from zero, and added to c in fp32 (4e-7).
-template <int K, int NJ, int kStep, bool kAT, bool kBT>
-__device__ __forceinline__ void mm(float (&c)[2][NJ][4], const WarpTile &w, const float *A, int lda, const float *B, int ldb) {
+template <int K, int kStep, bool kAT, bool kBT, int MI, int NJ>
+__device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, const float *A, int lda, const float *B, int ldb) {
 #pragma unroll 1
     for (int kb = 0; kb < K; kb += 16) {
-        float sum[2][NJ][4];
+        float sum[MI][NJ][4];
 #pragma unroll
         for (int kk = 0; kk < 16; kk += 8) {
             const int k0 = kb + kk;
-            uint32_t ah[2][4], al[2][4];
+            uint32_t ah[MI][4], al[MI][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int m = w.m0 + 16 * i + w.g + 8 * (e & 1), k = k0 + w.t + 4 * (e >> 1);
@@ -75,7 +77,7 @@ __device__ __forceinline__ void mm(float (&c)[2][NJ][4], const WarpTile &w, cons
                     split_tf32(kBT ? B[n * ldb + k] : B[k * ldb + n], bh[e], bl[e]);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < MI; ++i) {
                     if (kk == 0) sum[i][j][0] = sum[i][j][1] = sum[i][j][2] = sum[i][j][3] = 0.f;
                     mma_tf32(sum[i][j], al[i], bh);
                     mma_tf32(sum[i][j], ah[i], bl);
@@ -84,17 +86,17 @@ __device__ __forceinline__ void mm(float (&c)[2][NJ][4], const WarpTile &w, cons
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) c[i][j][e] += sum[i][j][e];
     }
 }
-template <int NJ>
-__device__ __forceinline__ void zero(float (&c)[2][NJ][4]) {
+template <int MI, int NJ>
+__device__ __forceinline__ void zero(float (&c)[MI][NJ][4]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -121,14 +123,14 @@ __device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y) {
 
 // Columns [c0, c0 + W) of a chunk's rows of a [tokens, H, D] tensor, in two steps: read into registers (zeros from row
 // Lc on), and written to shared memory.
-template <typename Tin, int D, int W>
+template <typename Tin, int D, int W, int kThreads = NT>
 struct TileRegs {
-    static constexpr int N = (C * (W / 4) + NT - 1) / NT;
+    static constexpr int N = (C * (W / 4) + kThreads - 1) / kThreads;
     float4 x[N];
     __device__ __forceinline__ void load(const void *src, long long row0, int H, int h, int c0, int Lc) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int idx = threadIdx.x + NT * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
+            const int idx = threadIdx.x + kThreads * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
             x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < Lc) x[i] = ld4(static_cast<const Tin *>(src) + ((size_t)(row0 + r) * H + h) * D + c0 + c);
         }
@@ -137,15 +139,15 @@ struct TileRegs {
     __device__ __forceinline__ void store(float *s, int lds, F f) const {  // f(row): a factor
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int idx = threadIdx.x + NT * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
+            const int idx = threadIdx.x + kThreads * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
             const float y = f(r);
             if (r < C) *reinterpret_cast<float4 *>(s + r * lds + c) = make_float4(y * x[i].x, y * x[i].y, y * x[i].z, y * x[i].w);
         }
     }
 };
-template <typename Tin, int D, int W>
+template <typename Tin, int D, int W, int kThreads = NT>
 __device__ __forceinline__ void load_tile(float *s, int lds, const void *src, long long row0, int H, int h, int c0, int Lc, float scale = 1.f) {
-    TileRegs<Tin, D, W> t;
+    TileRegs<Tin, D, W, kThreads> t;
     t.load(src, row0, H, h, c0, Lc);
     t.store(s, lds, [&](int) { return scale; });
 }
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[a][j][e] *= keep;
-            mm<C, NJ, 8 * WN, true, false>(x, w, sB, VP, sA, KP);
+            mm<C, 8 * WN, true, false>(x, w, sB, VP, sA, KP);
         }
         __syncthreads();  // the tiles are consumed
     }
@@ -291,17 +293,18 @@ __global__ void __launch_bounds__(256) hla_segment_scan_kernel(const HlaArgs p, 
 template <int DK, int DV>
 struct OutSmem {
     static constexpr int KP = DK + 4, VP = DV + 8;
-    // K's tile takes the state's tiles (JB rows of DK) once Q K^T is done
-    static constexpr int floats = 2 * C * KP + C * VP + C * LP;
+    // K's tile takes the state's tiles (64 rows of DK) once Q K^T is done, and then V: two CTAs to an SM
+    static constexpr int T = KP > VP ? KP : VP;
+    static constexpr int floats = C * KP + C * T + C * LP;
     static constexpr size_t bytes = sizeof(float) * floats + sizeof(float2) * C;
 };
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const uint8_t *__restrict__ gates, const float *__restrict__ Sc) {
+__global__ void __launch_bounds__(NT, 2) hla_out_simt_kernel(const HlaArgs p, const uint8_t *__restrict__ gates, const float *__restrict__ Sc) {
     using L = OutSmem<DK, DV>;
     constexpr int VJ = DV / 32;
     extern __shared__ __align__(16) float smem[];
-    float *sQ = smem, *sK = sQ + C * L::KP, *sV = sK + C * L::KP, *sP = sV + C * L::VP;
+    float *sQ = smem, *sK = sQ + C * L::KP, *sV = sK, *sP = sK + C * L::T;
     float2 *G = reinterpret_cast<float2 *>(sP + C * LP);
     const int h = blockIdx.x % p.H;
     const long long slot = blockIdx.x / p.H;
@@ -310,18 +313,17 @@ __global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const
     if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
     const long long row0 = sp.t0 + (long long)c * C;
     const int Lc = min(C, sp.len - c * C);
-    const WarpTile w = tile_2x4();
+    const WarpTile w = tile_of_warp<32>();
     const bool has_state = c > 0 || p.S0 != nullptr;
 
     load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc, p.scale);
     load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
-    load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
     if (threadIdx.x < C) G[threadIdx.x] = gate_of(gates, slot, p.H, h);
     __syncthreads();
     {
         float a[2][2][4];
         zero(a);
-        mm<DK, 2, 32, false, true>(a, w, sQ, L::KP, sK, L::KP);
+        mm<DK, 32, false, true>(a, w, sQ, L::KP, sK, L::KP);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const
             __syncthreads();
             float part[2][JT / 32][4];
             zero(part);
-            mm<DK, JT / 32, 32, false, true>(part, w, sQ, L::KP, sK, L::KP);
+            mm<DK, 32, false, true>(part, w, sQ, L::KP, sK, L::KP);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -369,7 +371,9 @@ __global__ void __launch_bounds__(NT) hla_out_simt_kernel(const HlaArgs p, const
                 }
             }
     }
-    mm<C, VJ, 32, false, false>(acc, w, sP, LP, sV, L::VP);
+    load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
+    __syncthreads();
+    mm<C, 32, false, false>(acc, w, sP, LP, sV, L::VP);
     Tin *o = static_cast<Tin *>(p.o);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -394,7 +398,7 @@ struct GradSmem {
 };
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, const uint8_t *__restrict__ gates, const float *__restrict__ Sc,
+__global__ void __launch_bounds__(NG) hla_grad_simt_kernel(const HlaArgs p, const uint8_t *__restrict__ gates, const float *__restrict__ Sc,
                                                            const float *__restrict__ Rc) {
     using L = GradSmem<DK, DV>;
     constexpr int KJ = DK / 32, VJ = DV / 32;
@@ -411,18 +415,18 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
     const long long row0 = sp.t0 + (long long)c * C;
     const int Lc = min(C, sp.len - c * C);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wn = warp & 3;
-    const WarpTile w = tile_2x4();
+    const WarpTile w = tile_of_warp<16>();
     const float2 g0 = make_float2(0.f, 0.f);
 
-    load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc);
-    load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
-    load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
-    load_tile<Tin, DV, DV>(sO, L::VP, p.dO, row0, p.H, h, 0, Lc, p.scale);
+    load_tile<Tin, DK, DK, NG>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc);
+    load_tile<Tin, DK, DK, NG>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
+    load_tile<Tin, DV, DV, NG>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
+    load_tile<Tin, DV, DV, NG>(sO, L::VP, p.dO, row0, p.H, h, 0, Lc, p.scale);
     if (threadIdx.x < C) G[threadIdx.x] = gate_of(gates, slot, p.H, h);
     __syncthreads();
 
     // the parts that go through the states: dQ from S_in, dK and dV from R, and their terms of dg
-    float dq[2][KJ][4], dk[2][KJ][4], dv[2][VJ][4];
+    float dq[1][KJ][4], dk[1][KJ][4], dv[1][VJ][4];
     zero(dq);
     zero(dk);
     float thr = 0.f;
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
     float *sS = sX, *sR = sX + JB * L::KP;
 #pragma unroll
     for (int jb = 0; jb < DV / JB; ++jb) {
-        for (int idx = threadIdx.x; idx < JB * (DK / 4); idx += NT) {
+        for (int idx = threadIdx.x; idx < JB * (DK / 4); idx += NG) {
             const int r = idx / (DK / 4), cc = 4 * (idx % (DK / 4));
             const float4 s4 = ld4(Sc + xb + (size_t)(jb * JB + r) * DK + cc), r4 = ld4(Rc + xb + (size_t)(jb * JB + r) * DK + cc);
             *reinterpret_cast<float4 *>(sS + r * L::KP + cc) = s4;
@@ -438,19 +442,19 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
             thr = fmaf(s4.x, r4.x, fmaf(s4.y, r4.y, fmaf(s4.z, r4.z, fmaf(s4.w, r4.w, thr))));
         }
         __syncthreads();
-        mm<JB, KJ, 32, false, false>(dq, w, sO + jb * JB, L::VP, sS, L::KP);
-        mm<JB, KJ, 32, false, false>(dk, w, sV + jb * JB, L::VP, sR, L::KP);
-        float part[2][1][4];
+        mm<JB, 32, false, false>(dq, w, sO + jb * JB, L::VP, sS, L::KP);
+        mm<JB, 32, false, false>(dk, w, sV + jb * JB, L::VP, sR, L::KP);
+        float part[1][1][4];
         zero(part);
-        mm<DK, 1, 32, false, true>(part, w, sK, L::KP, sR, L::KP);
+        mm<DK, 32, false, true>(part, w, sK, L::KP, sR, L::KP);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 1; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) dv[i][jb][e] = part[i][0][e];
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 1; ++i)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
             const int r = w.row(i, e);
@@ -487,13 +491,13 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
 
     // A = Q K^T . D, dA = dO' V^T . D, and the pairs within the chunk E = A . dO' V^T below the diagonal
     {
-        float a[2][2][4], da[2][2][4];
+        float a[1][2][4], da[1][2][4];
         zero(a);
         zero(da);
-        mm<DK, 2, 32, false, true>(a, w, sQ, L::KP, sK, L::KP);
-        mm<DV, 2, 32, false, true>(da, w, sO, L::VP, sV, L::VP);
+        mm<DK, 32, false, true>(a, w, sQ, L::KP, sK, L::KP);
+        mm<DV, 32, false, true>(da, w, sO, L::VP, sV, L::VP);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 1; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -507,12 +511,12 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
                 }
     }
     __syncthreads();
-    mm<C, KJ, 32, false, false>(dq, w, sD, LP, sK, L::KP);
-    mm<C, KJ, 32, true, false>(dk, w, sD, LP, sQ, L::KP);
-    mm<C, VJ, 32, true, false>(dv, w, sA, LP, sO, L::VP);
+    mm<C, 32, false, false>(dq, w, sD, LP, sK, L::KP);
+    mm<C, 32, true, false>(dk, w, sD, LP, sQ, L::KP);
+    mm<C, 32, true, false>(dv, w, sA, LP, sO, L::VP);
     Tin *out_q = static_cast<Tin *>(p.dq), *out_k = static_cast<Tin *>(p.dk_), *out_v = static_cast<Tin *>(p.dv_);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 1; ++i)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
             const int r = w.row(i, e);
@@ -541,8 +545,8 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = ty + 16 * i;
+    for (int i = 0; i < 2; ++i) {
+        const int t = ty + 32 * i;
         float u = 0.f;
         for (int s = tx; s < t; s += 16) u += sX[t * LP + s];
 #pragma unroll
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(NT) hla_grad_simt_kernel(const HlaArgs p, cons
         if (lane == 31) later = 0.f;
         if (lane == 0) earlier = 0.f;
 #pragma unroll
-        for (int k = 0; k < NT / 32; ++k) through += sThr[k];
+        for (int k = 0; k < NG / 32; ++k) through += sThr[k];
         through *= hla_decay(G[C - 1], g0);
         Tin *dg = static_cast<Tin *>(p.dg);
         if (t < Lc) st_elem(dg, (size_t)(row0 + t) * p.H + h, (sWith[t] + ((rd[0] + rd[1]) + later)) + (earlier + through));
@@ -682,7 +686,7 @@ cudaError_t backward_t(const HlaArgs &a) {
     constexpr size_t bytes = GradSmem<DK, DV>::bytes;
     static HlaSmem smem;
     if ((e = smem.raise(kern, bytes)) != cudaSuccess) return e;
-    kern<<<(unsigned)(l.slots * a.H), NT, bytes, a.stream>>>(a, s.gates, s.X[0], s.X[1]);
+    kern<<<(unsigned)(l.slots * a.H), NG, bytes, a.stream>>>(a, s.gates, s.X[0], s.X[1]);
     return cudaGetLastError();
 }
 
