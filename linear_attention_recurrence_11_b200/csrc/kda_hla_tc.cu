@@ -44,7 +44,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
 
 constexpr uint32_t GATE = kHlaGateBytes<C>;
 
-// Masked decayed scores of one TMEM row r (in the 32 rows from R on) and the 32 columns from `col` on, in bf16 pairs:
+// Masked decayed scores of one TMEM row r (in the 32 rows from R on), 16 columns at a time:
 // x D_rs, D_rs = 2^{G_r - G_s} for s <= r, and 0 above. Columns that all come before these rows take D_rs as
 // 2^{G_r - G_e} F_s, e the last of the columns: both factors are at most 1, the second is the same for all rows, and a
 // product replaces the exponential (5 instructions an element instead of 12).
@@ -54,22 +54,19 @@ struct DecayRow {
     float2 gr;
     int r, R, Lc;
     float scale;
-    // the decays of columns col + 16 q .. + 15, times scale; zero where masked
-    __device__ __forceinline__ bool none(int col) const { return col > R; }
-    __device__ __forceinline__ void get(int col, int q, float (&d)[16]) const {
+    // the decays of 16 columns, times scale; zero where masked
+    __device__ __forceinline__ bool none(int col) const { return col > R + 31; }
+    __device__ __forceinline__ void get(int col, float (&d)[16]) const {
         if (col < R) {
-            const float x = r < Lc ? scale * hla_decay(gr, G[col + 31]) : 0.f;
+            const float x = r < Lc ? scale * hla_decay(gr, G[col | 31]) : 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(F + col + 16 * q + e);
+                const float4 f = *reinterpret_cast<const float4 *>(F + col + e);
                 d[e] = x * f.x; d[e + 1] = x * f.y; d[e + 2] = x * f.z; d[e + 3] = x * f.w;
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int s = col + 16 * q + e;
-                d[e] = s <= r && r < Lc ? scale * hla_decay(gr, G[s]) : 0.f;
-            }
+            for (int e = 0; e < 16; ++e) d[e] = col + e <= r && r < Lc ? scale * hla_decay(gr, G[col + e]) : 0.f;
         }
     }
     // x d with the masked elements dropped, not multiplied: they may be anything
@@ -213,7 +210,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (tok < Lc) {
                 const float2 gt = G(i)[tok];
                 const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(G(i)[C - 1], gt);
-#pragma unroll
+#pragma unroll 2
                 for (int q = 0; q < NX / 8; ++q) {
                     const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
                     const uint4 v = *reinterpret_cast<const uint4 *>(ra + off);
@@ -250,28 +247,24 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (!ok) break;
             tc_fence_after();
             const DecayRow dr{G(i), reinterpret_cast<const float *>(G(i) + C), G(i)[r], r, R, Lc, p.scale};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int col = 64 * half + 32 * k;
-                float w[16];  // bf16 pairs
+            // (a loop of 16 columns, not unrolled: the warps' roles are long straight lines of code, and what is not
+            // fetched again runs at a third of the rate)
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int col = 64 * half + 16 * k;
+                uint32_t w[8];  // bf16 pairs
                 if (dr.none(col)) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = 0.f;
+                    for (int e = 0; e < 8; ++e) w[e] = 0u;
                 } else {
+                    float v[16], d[16];
+                    tmem_ld16(tmem + tlane + TS + col, v);
+                    dr.get(col, d);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float v[16], d[16];
-                        tmem_ld16(tmem + tlane + TS + col + 16u * q, v);
-                        dr.get(col, q, d);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int c = col + 16 * q + 2 * e;
-                            w[8 * q + e] = __uint_as_float(pack_bf2(dr.keep(c, v[2 * e], d[2 * e]), dr.keep(c + 1, v[2 * e + 1], d[2 * e + 1])));
-                        }
-                    }
+                    for (int e = 0; e < 8; ++e) w[e] = pack_bf2(dr.keep(col + 2 * e, v[2 * e], d[2 * e]), dr.keep(col + 2 * e + 1, v[2 * e + 1], d[2 * e + 1]));
                 }
-                tmem_st16(tmem + tlane + TP + 32u * half + 16u * k, w);
+                tmem_st8(tmem + tlane + TP + 32u * half + 8u * k, w);
             }
             tmem_wait_st();
             done(D_P);
@@ -735,7 +728,7 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
                 float a[16], d[16], f[16];
                 tmem_ld16(tmem + tlane + T0 + col + 16u * q, a);
                 tmem_ld16(tmem + tlane + T1 + col + 16u * q, d);
-                dr.get(col, q, f);
+                dr.get(col + 16 * q, f);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
