@@ -210,7 +210,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (tok < Lc) {
                 const float2 gt = G(i)[tok];
                 const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(G(i)[C - 1], gt);
-#pragma unroll 2
+#pragma unroll 1
                 for (int q = 0; q < NX / 8; ++q) {
                     const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
                     const uint4 v = *reinterpret_cast<const uint4 *>(ra + off);
@@ -319,7 +319,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (!wait(C_QS, i)) break;
                 tc_fence_after();
                 const float since = p.scale * hla_decay(G(i)[r], g0);
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < NO / 16; ++q) {
                     float v[16];
                     tmem_ld16(tmem + tlane + TO + oc + 16u * q, v);
@@ -356,7 +356,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             // costs the LSU four times the full tile's
             const int Lc = rows_of(i);
             uint8_t *stage = sm + L::O + (warp - 8) * 2 * KB;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < NO / 32; ++k) {
                 const int c = oc + 32 * k;
                 float v[32];
