@@ -122,13 +122,13 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
-    // every barrier completes once per chunk: its phase is the chunk's parity
-    // (the loads': once per tile buffer, of which the states' kernels have two)
-    constexpr int NS = kMode == kOut ? 1 : 2;
-    enum { F_K, F_V = F_K + 2, F_Q = F_V + 2,  // tiles have arrived (a's with the gates)
-           D_SCALE = F_Q + 1, D_P, D_X, D_S, D_O, D_E,  // done: hi + lo; scores; increment read; operand; Q S scaled; outputs read
-           C_QK, C_X, C_QS, C_PV, C_END,     // products
-           R_S = F_Q,                         // kStates: the operand tile has been read by its store
+    // A barrier completes once per chunk, its phase is the chunk's parity; one that is waited for two chunks later
+    // is a pair, of which a chunk takes one: a phase can only be told from the next, not from the one after.
+    constexpr int NS = kMode == kOut ? 1 : 2;  // buffers of a and b
+    enum { F_K, F_V = F_K + 2, F_Q = F_V + 2,   // tiles have arrived, by buffer (a's with the gates)
+           D_SCALE = F_Q + 1, D_P, D_X, D_S, D_O, D_E,  // done: hi + lo; scores; increment read; operand; Q S scaled; outputs read (pair)
+           C_QK = D_E + 2, C_QS, C_PV, C_X, C_END = C_X + 2,  // products (increment: a pair)
+           R_S = F_Q,                           // kStates: the operand tile has been read by its store
            NBAR = C_END + 1 };
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + NBAR);
 
@@ -160,7 +160,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const float2 g0 = make_float2(0.f, 0.f);
 
     if (tid == 0) {
-        for (int i = 0; i < NBAR; ++i) mbar_init(bars + i, i >= D_SCALE && i <= D_E ? 8 : 1);
+        for (int i = 0; i < NBAR; ++i) mbar_init(bars + i, i >= D_SCALE && i < C_QK ? 8 : 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -172,7 +172,8 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    constexpr uint32_t TX = 0, TO = 128, TS = 256, TP = 384;  // increment, outputs, scores, bf16 scores
+    // increment; outputs (of two chunks); scores, and in bf16, each half in the first half of its columns
+    constexpr uint32_t TX = 0, TO = 128, TS = 384;
 
     bool ok = true;
     const auto wait = [&](int b, int i) {  // (by a warp that goes on or gives up as one, or by one thread)
@@ -180,7 +181,8 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (warp < 16) ok = __all_sync(0xffffffffu, ok);
         return ok;
     };
-    const auto wait_tile = [&](int b, int i) { return NS == 1 ? wait(b, i) : wait(b + (i & 1), i >> 1); };
+    const auto wait_pair = [&](int b, int i) { return wait(b + (i & 1), i >> 1); };
+    const auto wait_tile = [&](int b, int i) { return NS == 1 ? wait(b, i) : wait_pair(b, i); };
     // a warp's threads have done their part: their writes to shared memory and TMEM are seen by what waits on b
     const auto done = [&](int b) {
         fence_proxy_async_smem();
@@ -200,7 +202,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int Lc = rows_of(i);
             wait_tile(F_K, i);
             if (Lc < C) wait_tile(F_V, i);
-            if (i > 0) wait(C_X, i - 1);  // hi and lo are read
+            if (i > 0) wait_pair(C_X, i - 1);  // hi and lo are read
             if (!ok) break;
             // a row times its weight, as hi + lo; a row behind the sequence's end is zero on both sides of
             // the products (what stands there may be anything)
@@ -242,9 +244,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             done(D_SCALE);
             if (kMode != kOut) continue;
-            wait(C_QK, i);
-            if (i > 0) wait(C_PV, i - 1);  // the bf16 scores are read
-            if (!ok) break;
+            if (!wait(C_QK, i)) break;
             tc_fence_after();
             const DecayRow dr{G(i), reinterpret_cast<const float *>(G(i) + C), G(i)[r], r, R, Lc, p.scale};
             // (a loop of 16 columns, not unrolled: the warps' roles are long straight lines of code, and what is not
@@ -264,7 +264,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = pack_bf2(dr.keep(col + 2 * e, v[2 * e], d[2 * e]), dr.keep(col + 2 * e + 1, v[2 * e + 1], d[2 * e + 1]));
                 }
-                tmem_st8(tmem + tlane + TP + 32u * half + 8u * k, w);
+                tmem_st8(tmem + tlane + TS + 64u * half + 8u * k, w);
             }
             tmem_wait_st();
             done(D_P);
@@ -319,19 +319,20 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 if (!wait(C_QS, i)) break;
                 tc_fence_after();
                 const float since = p.scale * hla_decay(G(i)[r], g0);
+                const uint32_t to = tmem + tlane + TO + 128u * (i & 1) + oc;
 #pragma unroll 1
                 for (int q = 0; q < NO / 16; ++q) {
                     float v[16];
-                    tmem_ld16(tmem + tlane + TO + oc + 16u * q, v);
+                    tmem_ld16(to + 16u * q, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] *= since;
-                    tmem_st16(tmem + tlane + TO + oc + 16u * q, v);
+                    tmem_st16(to + 16u * q, v);
                 }
                 tmem_wait_st();
                 done(D_O);
             }
-            if (!wait(C_X, i)) break;
+            if (!wait_pair(C_X, i)) break;
             tc_fence_after();
             const float keep = hla_decay(G(i)[C - 1], g0);
             total *= keep;
@@ -360,7 +361,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int k = 0; k < NO / 32; ++k) {
                 const int c = oc + 32 * k;
                 float v[32];
-                tmem_ld32(tmem + tlane + TO + c, v);
+                tmem_ld32(tmem + tlane + TO + 128u * (i & 1) + c, v);
                 tmem_wait_ld();
                 uint4 w[4];
 #pragma unroll
@@ -385,7 +386,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     for (int e = 0; e < 4; ++e) dst[e] = w[e];
                 }
             }
-            done(D_E);
+            done(D_E + (i & 1));
         }
         if (ok && end && r < p.dv) {
 #pragma unroll
@@ -404,15 +405,17 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int i = 0; i < nc && ok; ++i) {
                 if (kMode == kOut) {
                     wait(F_K, i);
-                    if (!wait(F_Q, i)) break;
-                    tc_fence_after();
-                    mma_chain<DKP / 16>(tmem + TS, oQ, oK, idS, false);  // (D_P of the chunk before: its scores are read)
-                    mma_commit(bars + C_QK);
-                    wait(D_S, i);
-                    if (i > 0) wait(D_E, i - 1);
+                    wait(F_Q, i);
+                    if (i > 0) wait(C_PV, i - 1);  // the bf16 scores before, which these replace, are read
                     if (!ok) break;
                     tc_fence_after();
-                    mma_chain<DKP / 16>(tmem + TO, oQ, oS, idO, false);
+                    mma_chain<DKP / 16>(tmem + TS, oQ, oK, idS, false);
+                    mma_commit(bars + C_QK);
+                    wait(D_S, i);
+                    if (i > 1) wait_pair(D_E, i - 2);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_chain<DKP / 16>(tmem + TO + 128u * (i & 1), oQ, oS, idO, false);
                     mma_commit(bars + C_QS);
                 }
                 wait(D_SCALE, i);
@@ -425,14 +428,15 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const Opnd oVt{vb, true, 0, DVP == 128 ? TILE : 0u};
                 mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::HI + st * L::KT, true, 0, TILE}, idX, false);
                 mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::LO, true, 0, TILE}, idX, true);
-                mma_commit(bars + C_X);
+                mma_commit(bars + C_X + (i & 1));
                 if (kMode == kOut) {
                     wait(D_P, i);
                     if (!wait(D_O, i)) break;
                     tc_fence_after();
                     const uint64_t dV = smem_desc_sw128(vb, TILE, 1024u);
 #pragma unroll
-                    for (int k = 0; k < C / 16; ++k) mma_bf16_ts(tmem + TO, tmem + TP + 8u * k, dV + (uint64_t)((k * 2048u) >> 4), idP, 1u);
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_bf16_ts(tmem + TO + 128u * (i & 1), tmem + TS + 64u * (k >> 2) + 8u * (k & 3), dV + (uint64_t)((k * 2048u) >> 4), idP, 1u);
                     mma_commit(bars + C_PV);
                 }
             }
@@ -451,11 +455,10 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         wait(C_QK, i - 1);
                     }
                 } else if (i > 1) {
-                    wait(C_X, i - 2);
-                    wait(D_X, i - 2);  // (the gates' ring)
+                    wait_pair(C_X, i - 2);
                 }
-                // The gates' ring: what reads chunk i - 4's is done, before chunk i - 2's D_O that Q K^T of chunk i - 1
-                // was issued after, or before its D_X.
+                // (The gates' ring: what reads chunk i - 4's was done before D_O of chunk i - 2, which came before Q K^T of
+                // chunk i - 1; or, without outputs, before D_X of chunk i - 3, which came before the increment of chunk i - 2.)
                 if (!ok) break;
                 mbar_arrive_expect_tx(bars + F_K + st, L::KT + GATE);
                 ++nk;
