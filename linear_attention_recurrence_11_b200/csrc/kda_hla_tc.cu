@@ -46,8 +46,9 @@ constexpr uint32_t GATE = kHlaGateBytes<C>;
 
 // Masked decayed scores of one TMEM row r (in the 32 rows from R on), 16 columns at a time:
 // x D_rs, D_rs = 2^{G_r - G_s} for s <= r, and 0 above. Columns that all come before these rows take D_rs as
-// 2^{G_r - G_e} F_s, e the last of the columns: both factors are at most 1, the second is the same for all rows, and a
-// product replaces the exponential (5 instructions an element instead of 12).
+// 2^{G_r - G_e} F_s, e the last of the 32 columns: both factors are at most 1, the second is the same for all rows, and
+// a product replaces the exponential (5 instructions an element instead of 12). On the diagonal the first factor is
+// 1 or more; it and F_s keep their precision as long as these 32 tokens together decay by less than 2^-60.
 struct DecayRow {
     const float2 *G;
     const float *F;
@@ -57,7 +58,7 @@ struct DecayRow {
     // the decays of 16 columns, times scale; zero where masked
     __device__ __forceinline__ bool none(int col) const { return col > R + 31; }
     __device__ __forceinline__ void get(int col, float (&d)[16]) const {
-        if (col < R) {
+        if (col < R || G[col & ~31].x - G[col | 31].x <= 60.f) {
             const float x = r < Lc ? scale * hla_decay(gr, G[col | 31]) : 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
