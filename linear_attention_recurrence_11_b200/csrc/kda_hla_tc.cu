@@ -100,12 +100,14 @@ struct ChainArgs {
 };
 
 // Outputs: one tile each of a, its hi and lo halves, b, q, the state, and the outputs' staging. States: two of a, whose hi
-// halves replace it, and two of b.
+// halves replace it, two of lo, so that a chunk is scaled while the one before is multiplied (2.0 us a chunk where one
+// took 2.2), and what else fits: one of b and the state, or two of b.
 template <int DKP, int DVP, int kMode>
 struct ChainSmem {
     static constexpr bool out = kMode == kOut;
     static constexpr uint32_t KT = (DKP / 64) * TILE, VT = (DVP / 64) * TILE;
-    static constexpr uint32_t K = 0, HI = out ? KT : 0u, LO = 2 * KT, V = 3 * KT, S = V + (out ? 1 : 2) * VT, Q = S + DKP * DVP * 2;
+    static constexpr int NK = out ? 1 : 2, NV = kMode == kEnds ? 2 : 1;  // buffers of a (and of lo), of b
+    static constexpr uint32_t K = 0, HI = out ? KT : 0u, LO = 2 * KT, V = LO + NK * KT, S = V + NV * VT, Q = S + (kMode == kEnds ? 0 : DKP * DVP * 2);
     static constexpr uint32_t O = Q + (out ? KT : 0u);             // 8 warps x 32 rows of 32 columns
     static constexpr uint32_t G = O + (out ? 16 * KB : 0u), BARS = G + 4 * GATE;  // a ring of four chunks' gates
     static constexpr uint32_t bytes = BARS + 256 + 1024;           // slack for 1024-byte alignment
@@ -125,9 +127,9 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
     // A barrier completes once per chunk, its phase is the chunk's parity; one that is waited for two chunks later
     // is a pair, of which a chunk takes one: a phase can only be told from the next, not from the one after.
-    constexpr int NS = kMode == kOut ? 1 : 2;  // buffers of a and b
+    constexpr int NK = L::NK, NV = L::NV;
     enum { F_K, F_V = F_K + 2, F_Q = F_V + 2,   // tiles have arrived, by buffer (a's with the gates)
-           D_SCALE = F_Q + 1, D_P, D_X, D_S, D_O, D_E,  // done: hi + lo; scores; increment read; operand; Q S scaled; outputs read (pair)
+           D_SCALE = F_Q + 1, D_P = D_SCALE + 2, D_X, D_S, D_O, D_E,  // done: hi + lo (pair); scores; increment read; operand; Q S scaled; outputs read (pair)
            C_QK = D_E + 2, C_QS, C_PV, C_X, C_END = C_X + 2,  // products (increment: a pair)
            R_S = F_Q,                           // kStates: the operand tile has been read by its store
            NBAR = C_END + 1 };
@@ -183,7 +185,11 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         return ok;
     };
     const auto wait_pair = [&](int b, int i) { return wait(b + (i & 1), i >> 1); };
-    const auto wait_tile = [&](int b, int i) { return NS == 1 ? wait(b, i) : wait_pair(b, i); };
+    const auto wait_k = [&](int i) { return NK == 1 ? wait(F_K, i) : wait_pair(F_K, i); };
+    const auto wait_v = [&](int i) { return NV == 1 ? wait(F_V, i) : wait_pair(F_V, i); };
+    // buffer of chunk i
+    const auto k_of = [&](int i) { return NK == 1 ? 0u : (uint32_t)(i & 1); };
+    const auto v_of = [&](int i) { return NV == 1 ? 0u : (uint32_t)(i & 1); };
     // a warp's threads have done their part: their writes to shared memory and TMEM are seen by what waits on b
     const auto done = [&](int b) {
         fence_proxy_async_smem();
@@ -201,15 +207,18 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const int tok = tid & 127, blk = DKP == 128 ? tid >> 7 : 0, q0 = DKP == 128 ? 0 : 4 * (tid >> 7);
         for (int i = 0; i < nc && ok; ++i) {
             const int Lc = rows_of(i);
-            wait_tile(F_K, i);
-            if (Lc < C) wait_tile(F_V, i);
-            if (i > 0) wait_pair(C_X, i - 1);  // hi and lo are read
+            wait_k(i);
+            if (i >= NK) wait_pair(C_X, i - NK);  // hi and lo are read
+            if (Lc < C) {  // b's tile is waited for here only, so first what its buffer's load before was there for
+                if (i >= NV) wait_pair(C_X, i - NV);
+                wait_v(i);
+            }
             if (!ok) break;
             // a row times its weight, as hi + lo; a row behind the sequence's end is zero on both sides of
             // the products (what stands there may be anything)
-            const uint32_t kt = NS == 1 ? 0u : (i & 1) * L::KT;
+            const uint32_t kt = k_of(i) * L::KT;
             const uint8_t *ra = sm + L::K + kt + blk * TILE;
-            uint8_t *rh = sm + L::HI + kt + blk * TILE, *rl = sm + L::LO + blk * TILE;
+            uint8_t *rh = sm + L::HI + kt + blk * TILE, *rl = sm + L::LO + kt + blk * TILE;
             if (tok < Lc) {
                 const float2 gt = G(i)[tok];
                 const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(G(i)[C - 1], gt);
@@ -240,10 +249,10 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int b = 0; b < DVP / 64; ++b)
-                        *reinterpret_cast<uint4 *>(sm + L::V + (NS == 1 ? 0u : (i & 1) * L::VT) + b * TILE +
+                        *reinterpret_cast<uint4 *>(sm + L::V + v_of(i) * L::VT + b * TILE +
                                                     sw128_offset(tok, 8 * (4 * (tid >> 7) + q))) = z;
             }
-            done(D_SCALE);
+            done(D_SCALE + (i & 1));
             if (kMode != kOut) continue;
             if (!wait(C_QK, i)) break;
             tc_fence_after();
@@ -419,16 +428,16 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     mma_chain<DKP / 16>(tmem + TO + 128u * (i & 1), oQ, oS, idO, false);
                     mma_commit(bars + C_QS);
                 }
-                wait(D_SCALE, i);
-                wait_tile(F_V, i);
+                wait_pair(D_SCALE, i);
+                wait_v(i);
                 if (i > 0) wait(D_X, i - 1);
                 if (!ok) break;
                 tc_fence_after();
                 // (a 64-row dv is read twice as the upper half of M: lanes that nothing reads)
-                const uint32_t st = NS == 1 ? 0u : (uint32_t)(i & 1), vb = sbase + L::V + st * L::VT;
+                const uint32_t kt = k_of(i) * L::KT, vb = sbase + L::V + v_of(i) * L::VT;
                 const Opnd oVt{vb, true, 0, DVP == 128 ? TILE : 0u};
-                mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::HI + st * L::KT, true, 0, TILE}, idX, false);
-                mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::LO, true, 0, TILE}, idX, true);
+                mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::HI + kt, true, 0, TILE}, idX, false);
+                mma_chain<C / 16>(tmem + TX, oVt, Opnd{sbase + L::LO + kt, true, 0, TILE}, idX, true);
                 mma_commit(bars + C_X + (i & 1));
                 if (kMode == kOut) {
                     wait(D_P, i);
@@ -449,10 +458,10 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             int nk = 0, nq = 0, nv = 0;  // loads issued
             for (int i = 0; i < nc && ok; ++i) {
                 const int tok = (int)row_of(i);
-                const uint32_t st = NS == 1 ? 0u : (uint32_t)(i & 1);
+                const uint32_t kb = k_of(i), vb = v_of(i);
                 if (kMode == kOut) {
                     if (i > 0) {
-                        wait(D_SCALE, i - 1);
+                        wait_pair(D_SCALE, i - 1);
                         wait(C_QK, i - 1);
                     }
                 } else if (i > 1) {
@@ -461,12 +470,12 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 // (The gates' ring: what reads chunk i - 4's was done before D_O of chunk i - 2, which came before Q K^T of
                 // chunk i - 1; or, without outputs, before D_X of chunk i - 3, which came before the increment of chunk i - 2.)
                 if (!ok) break;
-                mbar_arrive_expect_tx(bars + F_K + st, L::KT + GATE);
+                mbar_arrive_expect_tx(bars + F_K + kb, L::KT + GATE);
                 ++nk;
-                bulk_load(sm + L::G + (i & 3) * GATE, s.gates + ((size_t)(sp.slot + chunk(i)) * p.H + h) * GATE, GATE, bars + F_K + st);
+                bulk_load(sm + L::G + (i & 3) * GATE, s.gates + ((size_t)(sp.slot + chunk(i)) * p.H + h) * GATE, GATE, bars + F_K + kb);
 #pragma unroll
                 for (int b = 0; b < DKP / 64; ++b) {
-                    tma_load_3d(sm + L::K + st * L::KT + b * TILE, ta, bars + F_K + st, 64 * b, h, tok);
+                    tma_load_3d(sm + L::K + kb * L::KT + b * TILE, ta, bars + F_K + kb, 64 * b, h, tok);
                 }
                 if (kMode == kOut) {
                     if (i > 0 && !wait(C_QS, i - 1)) break;
@@ -478,22 +487,23 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     }
                     if (i > 0 && !wait(C_PV, i - 1)) break;  // (and the products before it)
                 }
-                mbar_arrive_expect_tx(bars + F_V + st, L::VT);
+                if (kMode == kStates && i > 0 && !wait_pair(C_X, i - 1)) break;
+                mbar_arrive_expect_tx(bars + F_V + vb, L::VT);
                 ++nv;
 #pragma unroll
                 for (int b = 0; b < DVP / 64; ++b) {
-                    tma_load_3d(sm + L::V + st * L::VT + b * TILE, tb, bars + F_V + st, 64 * b, h, tok);
+                    tma_load_3d(sm + L::V + vb * L::VT + b * TILE, tb, bars + F_V + vb, 64 * b, h, tok);
                 }
             }
             // nothing may be in flight when the CTA ends: the last loads into each buffer (bounded)
-            const auto drain = [&](int b, int issued) {
-                for (int st = 0; st < NS; ++st) {
-                    const int of = NS == 1 ? issued : (issued + 1 - st) / 2;  // loads into this buffer
+            const auto drain = [&](int b, int buffers, int issued) {
+                for (int st = 0; st < buffers; ++st) {
+                    const int of = buffers == 1 ? issued : (issued + 1 - st) / 2;  // loads into this buffer
                     if (of > 0) mbar_wait_bounded(bars + b + st, (uint32_t)(of - 1) & 1u, kWaitCycles);
                 }
             };
-            drain(F_K, nk);
-            drain(F_V, nv);
+            drain(F_K, NK, nk);
+            drain(F_V, NV, nv);
             if (nq > 0) mbar_wait_bounded(bars + F_Q, (uint32_t)(nq - 1) & 1u, kWaitCycles);
         }
         __syncwarp();
