@@ -174,7 +174,7 @@ struct StateTile {
 };
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(NT) hla_state_simt_kernel(const StateArgs s) {
+__global__ void __launch_bounds__(NT, 2) hla_state_simt_kernel(const StateArgs s) {
     using L = StateTile<DK, DV>;
     constexpr int KP = L::KP, VP = L::VP, WN = L::WN, NJ = L::NJ, ROWS = L::ROWS;
     const HlaArgs &p = s.a;
@@ -615,8 +615,8 @@ Layout layout(const HlaArgs &a, bool back) {
     Layout l{};
     const int dirs = back ? 2 : 1;
     const bool packed = a.cu_seqlens != nullptr;
-    // up to four state CTAs run on an SM
-    l.sc = hla_segment_chunks(a, C, (long long)a.N * a.H * ((a.dv + 63) / 64) * dirs, 4LL * device_sm_count());
+    // two state CTAs run on an SM (its registers)
+    l.sc = hla_segment_chunks(a, C, (long long)a.N * a.H * ((a.dv + 63) / 64) * dirs, 2LL * device_sm_count());
     l.slots = hla_slots(packed, a.N, a.T, C);
     l.seg_slots = l.sc ? hla_slots(packed, a.N, a.T, l.sc * C) : 0;
     size_t at = 0;
