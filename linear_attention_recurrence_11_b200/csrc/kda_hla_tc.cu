@@ -97,6 +97,9 @@ struct ChainArgs {
     uint8_t *blob[2];   // kStates, per direction: chunk operands [slot][H]
     HlaSegments seg;
     const int32_t *order;  // packed batches: sequences, longest first (null: as they come)
+    int h0, hn;            // heads of this launch
+    unsigned *next;        // the gradients' counter of tiles, set to `first` (null: no gradients)
+    unsigned first;
 };
 
 // Outputs: one tile each of a, its hi and lo halves, b, q, the state, and the outputs' staging. States: two of a, whose hi
@@ -137,8 +140,12 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int dir = kMode == kOut ? 0 : blockIdx.z;
-    const int h = blockIdx.x % p.H;
-    const long long su = blockIdx.x / p.H;  // sequence, or segment slot
+    const int h = s.h0 + blockIdx.x % s.hn;
+    const long long su = blockIdx.x / s.hn;  // sequence, or segment slot
+    if (kMode == kStates) {
+        grid_launch_dependents();  // (the gradients of another launch's heads)
+        if (s.next && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) *s.next = s.first;
+    }
     int n = (int)su, sg = 0;
     HlaSpan sp;
     if (s.seg.sc) {
@@ -523,10 +530,13 @@ struct TileArgs {
     const uint8_t *gates;
     const uint8_t *S, *R;   // the chunks' incoming states, and the gradients of their outgoing ones
     unsigned tiles;         // chunk slots x heads
+    unsigned split;         // of which these, of heads 0 .. h1 - 1, come first; the others' states may still be under way
+    int h1;
+    unsigned *next;         // the next tile that no CTA has taken
 };
 
-// All gradients of a (chunk, head), by 512 threads; one CTA per SM, which goes through its tiles with the next one's
-// copies under way: q and k as soon as their products are done, the rest as the places fall free. With P = Q K^T and dP = dO V^T (both [row r, column
+// All gradients of a (chunk, head), by 512 threads; one CTA per SM, which takes tiles from a counter, with the next
+// one's copies under way: q and k as soon as their products are done, the rest as the places fall free. With P = Q K^T and dP = dO V^T (both [row r, column
 // s], so that one decay D_rs serves both), A = scale P . D and dA = scale dP . D in bf16:
 //   dQ = dA K   + scale e^{G_r} dO S      accumulators T2
 //   dK = dA^T Q + e^{G_C - G_r} V R       T3
@@ -555,30 +565,30 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
     using L = GradTile<DKP, DVP>;
     const HlaArgs &p = t.a;
     struct Tile {
-        unsigned i;
         long long slot, row0;
         int h, Lc;
         bool hasS, hasR;
     };
-    // the first tile at or after i of this CTA's that has a chunk
-    const auto find = [&](unsigned i, Tile &x) {
-        for (; i < t.tiles; i += gridDim.x) {
-            int n, c;
-            HlaSpan sp;
-            x.slot = i / p.H;
-            if (!hla_chunk_of(p, x.slot, C, n, c, sp)) continue;
-            x.i = i;
-            x.h = i % p.H;
-            x.row0 = sp.t0 + (long long)c * C;
-            x.Lc = min(C, sp.len - c * C);
-            x.hasS = p.S0 != nullptr || c > 0;
-            x.hasR = p.dST != nullptr || c + 1 < sp.nch;
-            return true;
-        }
-        return false;
+    // tile i; false for one without a chunk
+    const auto tile = [&](unsigned i, Tile &x) {
+        int n, c;
+        HlaSpan sp;
+        const unsigned j = i < t.split ? i : i - t.split, heads = i < t.split ? t.h1 : p.H - t.h1;
+        x.slot = j / heads;
+        if (!hla_chunk_of(p, x.slot, C, n, c, sp)) return false;
+        x.h = (i < t.split ? 0 : t.h1) + j % heads;
+        x.row0 = sp.t0 + (long long)c * C;
+        x.Lc = min(C, sp.len - c * C);
+        x.hasS = p.S0 != nullptr || c > 0;
+        x.hasR = p.dST != nullptr || c + 1 < sp.nch;
+        return true;
     };
-    Tile cur;
-    if (!find(blockIdx.x, cur)) return;
+    // (by one thread) i, if it has a chunk, or else the next one taken that has
+    const auto settle = [&](unsigned i) {
+        for (Tile x; i < t.tiles && !tile(i, x);) i = atomicAdd(t.next, 1u);
+        return i;
+    };
+    __shared__ unsigned s_tile[2];  // the next tile, by parity
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
@@ -599,6 +609,10 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         __syncwarp();
         tmem_alloc(s_tmem, 512);
         tmem_relinquish();
+    }
+    if (tid == 64) {
+        s_tile[1] = settle(blockIdx.x);
+        s_tile[0] = settle(atomicAdd(t.next, 1u));
     }
     tc_fence_before();
     __syncthreads();
@@ -650,7 +664,13 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         if (x.hasS) bulk_prefetch_l2(t.S + at, L::SB);
         if (x.hasR) bulk_prefetch_l2(t.R + at, L::SB);
     };
-    if (copier) {
+    Tile cur;
+    bool more = s_tile[1] < t.tiles;
+    if (more) {
+        if (s_tile[1] >= t.split) grid_dependency_wait();
+        tile(s_tile[1], cur);
+    }
+    if (copier && more) {
         load_qk(cur, 0);
         load_o(cur);
         load_vsr(cur);
@@ -660,10 +680,17 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
     const Opnd oQ{sbase + L::Q, false, TILE, 0}, oK{sbase + L::K, false, TILE, 0}, oV{sbase + L::V, false, TILE, 0}, oO{sbase + L::O, false, TILE, 0};
     const auto zero16 = [&](uint32_t off) { *reinterpret_cast<uint4 *>(sm + off) = make_uint4(0, 0, 0, 0); };
     bool bad = false;
-    for (int it = 0;; ++it) {
-        Tile nxt;
-        const bool more = find(cur.i + gridDim.x, nxt);
+    for (int it = 0; more; ++it) {
         const uint32_t ph = it & 1;
+        Tile nxt = cur;
+        const unsigned ni = s_tile[ph];
+        more = ni < t.tiles;
+        if (more) {
+            if (ni >= t.split) grid_dependency_wait();
+            tile(ni, nxt);
+        }
+        unsigned after = 0;  // the tile after the next: taken here, looked at when it has arrived
+        if (tid == 64) after = more ? atomicAdd(t.next, 1u) : t.tiles;
         const int Lc = cur.Lc;
         const bool hasS = cur.hasS, hasR = cur.hasR;
         const float2 *G = reinterpret_cast<const float2 *>(sm + L::G + ph * GATE);
@@ -874,6 +901,7 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         // dg by one warp: what a token from t on reads of one before t. Within the chunk: the later rows' sums
         // q . dQ less the later columns' sums k . dK1 (pairs that both count, the diagonal among them, cancel; the
         // rows' sums hold the reads of S too); the earlier columns' k . dK2; and e^{G_C} <S, R>.
+        if (tid == 64) s_tile[ph ^ 1] = settle(after);  // (read behind the tile's last barrier)
         if (p.dg && warp == 2) {
             double a[4], b[4];  // (larger terms cancel: fp64, of a few hundred numbers)
 #pragma unroll
@@ -923,9 +951,9 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
             if (more) load_vsr(nxt);
         }
         __syncwarp();
-        if (!more) break;
         cur = nxt;
     }
+    grid_dependency_wait();  // whatever follows this launch follows the states' too
     if (bad) {  // leave nothing in flight behind: the copies, and whatever products were issued
         if (copier) {
             if (p.dev_status) atomicExch(p.dev_status, (int)KDA_ERR_TIMEOUT);
@@ -967,7 +995,7 @@ struct Layout {
     int sc;
     bool order;
     long long slots, seg_slots;
-    size_t order_at, gates, blob[2], seg[2], keep[2], bytes;
+    size_t order_at, next, gates, blob[2], seg[2], keep[2], bytes;
 };
 Layout layout(const HlaArgs &a, bool back) {
     Layout l{};
@@ -981,6 +1009,7 @@ Layout layout(const HlaArgs &a, bool back) {
     // more chains than SMs, of different lengths: the longest first
     l.order = packed && !l.sc && seq_order_bytes(a.N) > 0 && (long long)a.N * a.H * dirs > device_sm_count();
     l.order_at = take(l.order ? seq_order_bytes(a.N) : 0);
+    l.next = take(back ? sizeof(unsigned) : 0);
     l.gates = take((size_t)l.slots * a.H * GATE);
     for (int d = 0; d < dirs; ++d) {
         l.blob[d] = take(back ? (size_t)l.slots * a.H * blob_bytes(dkp, dvp) : 0);
@@ -1002,7 +1031,7 @@ cudaError_t chain(const ChainArgs &s, const Maps &m, const Layout &l, int dirs) 
     static HlaSmem smem;
     const cudaError_t e = smem.raise(kern, bytes);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)((l.sc ? l.seg_slots : s.a.N) * s.a.H), 1, dirs), kChainThreads, bytes, s.a.stream>>>(m.k, m.v, m.q, m.o, s);
+    kern<<<dim3((unsigned)((l.sc ? l.seg_slots : s.a.N) * s.hn), 1, dirs), kChainThreads, bytes, s.a.stream>>>(m.k, m.v, m.q, m.o, s);
     return cudaGetLastError();
 }
 
@@ -1024,6 +1053,7 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     s.a = a;
     if (back) s.a.ST = nullptr;
     s.seg.sc = l.sc;
+    s.hn = a.H;
     s.gates = ws + l.gates;
     for (int d = 0; d < dirs; ++d) {
         s.blob[d] = ws + l.blob[d];
@@ -1043,20 +1073,50 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
         if ((e = launch_hla_segment_scan(a, s.seg, l.sc * C, dirs)) != cudaSuccess) return e;
     }
     if (!back) return chain<DKP, DVP, kOut>(s, m, l, 1);
-    if ((e = chain<DKP, DVP, kStates>(s, m, l, 2)) != cudaSuccess) return e;
+    const auto kern = hla_grad_tc_kernel<DKP, DVP>;
+    constexpr size_t bytes = GradTile<DKP, DVP>::bytes;
+    static HlaSmem smem;
+    if ((e = smem.raise(kern, bytes)) != cudaSuccess) return e;
+    // Chains that fill the SMs once or more and then some of them once again leave the others without work meanwhile. Of
+    // a dense batch, whose chains are of one length, the heads of that last round are a launch of their own, and the
+    // gradients of the heads before run beside it (96 heads x 8192 tokens, 192 chains on 148 SMs: 658 us against 711).
+    const unsigned sms = (unsigned)device_sm_count();
+    const long long chains = (long long)a.N * a.H * dirs;
+    int h1 = a.H;
+    if (!a.cu_seqlens && !l.sc && chains > sms && chains % sms) h1 = (int)(chains / sms * sms / (a.N * dirs));
+    if (h1 == 0) h1 = a.H;
+    s.next = reinterpret_cast<unsigned *>(ws + l.next);
+    s.first = units < sms ? units : sms;
+    s.hn = h1;
+    if ((e = chain<DKP, DVP, kStates>(s, m, l, dirs)) != cudaSuccess) return e;
+    if (h1 < a.H) {
+        s.next = nullptr;
+        s.h0 = h1;
+        s.hn = a.H - h1;
+        if ((e = chain<DKP, DVP, kStates>(s, m, l, dirs)) != cudaSuccess) return e;
+    }
     TileArgs t{};
     t.a = a;
     t.gates = s.gates;
     t.S = s.blob[0];
     t.R = s.blob[1];
     t.tiles = units;
-    const auto kern = hla_grad_tc_kernel<DKP, DVP>;
-    constexpr size_t bytes = GradTile<DKP, DVP>::bytes;
-    static HlaSmem smem;
-    if ((e = smem.raise(kern, bytes)) != cudaSuccess) return e;
-    const unsigned sms = (unsigned)device_sm_count();
-    kern<<<units < sms ? units : sms, 512, bytes, a.stream>>>(m.q, m.k, m.v, m.o, m.dq, m.dk, m.dv, t);
-    return cudaGetLastError();
+    t.split = (unsigned)(l.slots * h1);
+    t.h1 = h1;
+    t.next = reinterpret_cast<unsigned *>(ws + l.next);
+    // The attribute lets the launch begin once every CTA of the one before has: without a split that would be the launch
+    // whose results are read, so there it is left out.
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(s.first);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = a.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = h1 < a.H ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, m.q, m.k, m.v, m.o, m.dq, m.dk, m.dv, t);
 }
 
 cudaError_t pass(const HlaArgs &a, bool back) {
@@ -1068,7 +1128,7 @@ cudaError_t pass(const HlaArgs &a, bool back) {
 }  // namespace
 
 bool hla_tc_supported(const HlaArgs &a) {
-    // one tile per (chunk slot, head, slice of a result), in a 31-bit grid
+    // one tile per (chunk slot, head), counted in 32 bits with what the CTAs take past the last one
     return a.dtype == KDA_DTYPE_BF16 && hla_slots(a.cu_seqlens != nullptr, a.N, a.T, C) <= 0x7fffffffLL / 2 / a.H;
 }
 size_t hla_tc_workspace(const HlaArgs &a, bool back) { return layout(a, back).bytes; }

@@ -281,5 +281,10 @@ __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t
     return row * 128u + ((((byte >> 4) ^ (row & 7u)) & 7u) << 4) + (byte & 15u);
 }
 
+// A launch that was allowed to begin before the one ahead of it in the stream has ended (programmatic serialization): the
+// one ahead says from when on, and this one waits for its end and its results.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace sm100
 }  // namespace kda

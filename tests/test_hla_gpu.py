@@ -93,6 +93,8 @@ SHAPES = [  # B, T, H, dk, dv, dtype, gate, S0
     (1, 161, 3, 64, 128, "bf16", "token", True),
     (2, 70, 2, 64, 64, "bf16", "token", True),
     (1, 90, 2, 32, 32, "bf16", "token", True),
+    (1, 150, 80, 64, 64, "bf16", "token", True),     # more chains in the backward pass than SMs, and not twice as many
+    (2, 129, 43, 128, 64, "bf16", "token", False),
 ]
 
 
@@ -133,6 +135,31 @@ def test_packed(K, dtype, d, lead, tail):
         if name != "dS0":
             assert (a[:, :lead] == 0).all() and (a[:, cu[-1]:] == 0).all()
     assert torch.equal(got[4][2], x["dS_T"][2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_sequence_of_nans_stays_alone(K, dtype):
+    """Sequences that share a tile with one that holds NaN and infinities keep their results, to the bit."""
+    lens = [70, 200, 1, 59]
+    cu = cu_of(lens)
+    x = inputs(1, cu[-1], 2, 64, 64, dtype, seed=27, N=len(lens))
+    want = run_forward(K, x, cu) + run_backward(K, x, cu)
+    for i, n in enumerate(("q", "k", "v", "do", "g")):
+        x[n][:, cu[1] + 20 * i:cu[2] - 3] = float("nan") if i % 2 else float("inf") if n != "g" else float("nan")
+    got = run_forward(K, x, cu) + run_backward(K, x, cu)
+    for a, b in zip(want, got):
+        for n in (0, 2, 3):
+            part = (lambda y: y[n]) if a.dtype == torch.float32 and a.shape[0] == len(lens) else (lambda y: y[:, cu[n]:cu[n + 1]])
+            assert torch.equal(part(a), part(b))
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 300), ("f32", 300), ("bf16", 5000)])
+def test_states_updated_in_place(K, dtype, T):
+    """S_T may be S0 itself."""
+    x = inputs(1, T, 2, 64, 64, dtype, seed=28)
+    o, S = run_forward(K, x)
+    o2, S2 = run_forward(K, x, S_T=x["S0"])
+    assert S2 is x["S0"] and torch.equal(S2, S) and torch.equal(o2, o)
 
 
 def test_packed_more_chains_than_sms(K):
