@@ -461,8 +461,8 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
  *            checked: g <= 0 (a positive g grows the state). A g below -138
  *            (-infinity too) empties the state.
  *   S0     : the states before the first token, or NULL (zeros). S_T: the
- *            states after the last token, or NULL. A sequence without tokens
- *            has S_T = S0.
+ *            states after the last token, or NULL; S_T may be S0 itself. A
+ *            sequence without tokens has S_T = S0.
  *   cu_seqlens : device int32 [num_seqs + 1] (B must be 1, T is the total) or
  *            NULL (num_seqs is then ignored). Tokens before the first or
  *            behind the last sequence are neither read nor written. Offsets
@@ -479,7 +479,10 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
  *
  * Arithmetic: sums, states and decays in fp32 (the decays' sums in 64 bits). The
  * tensor cores take the scores and the states as bf16 operands; the states
- * themselves are carried in fp32, to about 2^-18.
+ * themselves are carried in fp32, to about 2^-18. A NaN or an infinity among
+ * q, k, v or dO may reach any row of its chunk (128 tokens on the tensor cores,
+ * else 64), earlier ones too, and what follows from the state; other sequences
+ * and heads, and rows of no sequence, are not touched by it.
  *
  * kda_hla_backward: the gradients of q, k, v, g and S0 from dO, the outputs'
  * (dtype, [B, T, H, dv]), and dS_T, the last states' (fp32, or NULL: zeros).

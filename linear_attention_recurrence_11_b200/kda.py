@@ -793,6 +793,8 @@ def kda_rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "no
         at = [rot_dim * math.log(original_length / (2 * math.pi * b)) / (2 * math.log(base)) for b in (beta_fast, beta_slow)]
         lo, hi = max(0.0, math.floor(at[0])), min(rot_dim - 1.0, math.ceil(at[1]))
         keep = 1.0 - ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        if at[1] < 0:  # (no pair turns even beta_slow times)
+            keep = torch.zeros_like(keep)
         inv = inv / factor * (1.0 - keep) + inv * keep
         mscale = 0.1 * math.log(factor) + 1.0
     elif scaling not in ("none", "base"):

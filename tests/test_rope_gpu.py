@@ -164,6 +164,8 @@ def test_frequencies(K):
     assert abs(m - 1.2079441541679836) < 1e-12
     assert torch.equal(ramp[:8], base[:8]) and torch.allclose(ramp[-4:] * 8, base[-4:], rtol=1e-6)
     assert ((ramp[1:] <= ramp[:-1])).all()
+    short, _ = K.kda_rope_inv_freq(64, scaling="ramp", factor=8.0, original_length=6)  # no pair turns even once
+    assert torch.allclose(short * 8, base, rtol=1e-6)
     for bad in (dict(rot_dim=7), dict(rot_dim=8, scaling="no"), dict(rot_dim=8, scaling="ramp", factor=2.0), dict(rot_dim=8, factor=0.5)):
         with pytest.raises(ValueError):
             K.kda_rope_inv_freq(**bad)
