@@ -51,11 +51,13 @@ __device__ __forceinline__ WarpTile tile_of_warp() {
     return {kRows * (warp >> 2), 8 * (warp & 3), lane >> 2, lane & 3};
 }
 
-// c += A B over K. A is [m][k], or with kAT [k][m]; B is [k][n], or with kBT [n][k]. The matrix instructions cut their
+// c += A B over K. A is [m][k], or with kAT [k][m], the latter with kW times a weight of each k; B is [k][n], or with kBT
+// [n][k]. The matrix instructions cut their
 // sums off instead of rounding them: over K = 128 that alone came to 3e-6 of the result. So 16 of K at a time are summed
 // by them, from zero, and added to c in fp32 (4e-7).
-template <int K, int kStep, bool kAT, bool kBT, int MI, int NJ>
-__device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, const float *A, int lda, const float *B, int ldb) {
+template <int K, int kStep, bool kAT, bool kBT, bool kW = false, int MI, int NJ>
+__device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, const float *A, int lda, const float *B, int ldb,
+                                   const float *weight = nullptr) {
 #pragma unroll 1
     for (int kb = 0; kb < K; kb += 16) {
         float sum[MI][NJ][4];
@@ -68,7 +70,7 @@ __device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int m = w.m0 + 16 * i + w.g + 8 * (e & 1), k = k0 + w.t + 4 * (e >> 1);
-                    split_tf32(kAT ? A[k * lda + m] : A[m * lda + k], ah[i][e], al[i][e]);
+                    split_tf32((kW ? weight[k] : 1.f) * (kAT ? A[k * lda + m] : A[m * lda + k]), ah[i][e], al[i][e]);
                 }
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
@@ -110,8 +112,7 @@ __device__ __forceinline__ float2 gate_of(const uint8_t *gates, long long slot, 
     return __ldg(reinterpret_cast<const float2 *>(gates + ((size_t)slot * H + h) * GATE) + threadIdx.x);
 }
 
-// four consecutive elements (8- or 16-byte aligned)
-__device__ __forceinline__ float4 ld4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
+// four consecutive elements (8-byte aligned)
 __device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
     const uint2 r = __ldg(reinterpret_cast<const uint2 *>(p));
     const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&r.x));
@@ -123,35 +124,37 @@ __device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
 }
 
-// Columns [c0, c0 + W) of a chunk's rows of a [tokens, H, D] tensor, in two steps: read into registers (zeros from row
-// Lc on), and written to shared memory.
+// 16 bytes of fp32 to shared memory, asynchronously; zeros if not `there`
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }  // all but the last N groups
+
+// Columns [c0, c0 + W) of a chunk's rows of a [tokens, H, D] tensor as fp32 in shared memory, zeros from row Lc on: there
+// once the thread's copies have been waited for and the block has met. fp32 is copied asynchronously (through registers,
+// the state kernel's loads alone held a chunk up for 3000 of 11000 clocks); bf16 is converted on its way.
 template <typename Tin, int D, int W, int kThreads = NT>
-struct TileRegs {
-    static constexpr int N = (C * (W / 4) + kThreads - 1) / kThreads;
-    float4 x[N];
-    __device__ __forceinline__ void load(const void *src, long long row0, int H, int h, int c0, int Lc) {
+__device__ __forceinline__ void fetch_tile(float *s, int lds, const void *src, long long row0, int H, int h, int c0, int Lc) {
+    constexpr int N = C * (W / 4) / kThreads;
+    static_assert(N * kThreads == C * (W / 4), "whole rows of threads");
+    const Tin *base = static_cast<const Tin *>(src) + ((size_t)row0 * H + h) * D + c0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int idx = threadIdx.x + kThreads * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
-            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < Lc) x[i] = ld4(static_cast<const Tin *>(src) + ((size_t)(row0 + r) * H + h) * D + c0 + c);
-        }
+    for (int i = 0; i < N; ++i) {
+        const int idx = threadIdx.x + kThreads * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
+        const Tin *at = base + (r < Lc ? (size_t)r * H * D : 0) + c;
+        if constexpr (sizeof(Tin) == 4) copy16(s + r * lds + c, at, r < Lc);
+        else *reinterpret_cast<float4 *>(s + r * lds + c) = r < Lc ? ld4(at) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    template <typename F>
-    __device__ __forceinline__ void store(float *s, int lds, F f) const {  // f(row): a factor
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int idx = threadIdx.x + kThreads * i, r = idx / (W / 4), c = 4 * (idx % (W / 4));
-            const float y = f(r);
-            if (r < C) *reinterpret_cast<float4 *>(s + r * lds + c) = make_float4(y * x[i].x, y * x[i].y, y * x[i].z, y * x[i].w);
-        }
+}
+// `rows` rows of a state
+template <int D, int kThreads = NT>
+__device__ __forceinline__ void fetch_state(float *s, int lds, const float *src, int rows) {
+    for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
+        const int r = idx / (D / 4), c = 4 * (idx % (D / 4));
+        copy16(s + r * lds + c, src + (size_t)r * D + c, true);
     }
-};
-template <typename Tin, int D, int W, int kThreads = NT>
-__device__ __forceinline__ void load_tile(float *s, int lds, const void *src, long long row0, int H, int h, int c0, int Lc, float scale = 1.f) {
-    TileRegs<Tin, D, W, kThreads> t;
-    t.load(src, row0, H, h, c0, Lc);
-    t.store(s, lds, [&](int) { return scale; });
 }
 
 // ------------------------------------------------------------------- states
@@ -172,7 +175,7 @@ template <int DK, int DV>
 struct StateTile {
     static constexpr int ROWS = DV < 64 ? 32 : 64, WN = ROWS == 64 ? 4 : DK < 64 ? 4 : 8, NJ = DK / (8 * WN);
     static constexpr int KP = DK + 8, VP = ROWS + 8;  // (read down the columns: 8 mod 32)
-    static constexpr size_t bytes = sizeof(float) * C * (KP + VP) + sizeof(float2) * C;
+    static constexpr size_t bytes = sizeof(float) * (2 * C * (KP + VP) + 2 * (C + 4));  // two chunks' tiles, weights and decay
 };
 
 template <typename Tin, int DK, int DV>
@@ -181,8 +184,7 @@ __global__ void __launch_bounds__(NT, 2) hla_state_simt_kernel(const StateArgs s
     constexpr int KP = L::KP, VP = L::VP, WN = L::WN, NJ = L::NJ, ROWS = L::ROWS;
     const HlaArgs &p = s.a;
     extern __shared__ __align__(16) float smem[];
-    float *sA = smem, *sB = sA + C * KP;
-    float2 *G = reinterpret_cast<float2 *>(sB + C * VP);
+    float *sA = smem, *sB = sA + 2 * C * KP, *sW = sB + 2 * C * VP;
     const int dir = blockIdx.z, j0 = blockIdx.y * ROWS, h = blockIdx.x % p.H;
     const long long su = blockIdx.x / p.H;
     int n = (int)su, sg = 0;
@@ -219,32 +221,42 @@ __global__ void __launch_bounds__(NT, 2) hla_state_simt_kernel(const StateArgs s
         v = y.y;
     });
     const auto chunk = [&](int i) { return dir ? c1 - 1 - i : c0 + i; };
-    TileRegs<Tin, DK, DK> ta;
-    TileRegs<Tin, DV, ROWS> tb;
-    float2 gate;
-    const auto load = [&](int i) {
-        const int c = chunk(i), Lc = min(C, sp.len - c * C);
-        const long long row0 = sp.t0 + (long long)c * C;
-        if (threadIdx.x < C) gate = gate_of(s.gates, sp.slot + c, p.H, h);
-        ta.load(dir ? p.q : p.k, row0, p.H, h, 0, Lc);
-        tb.load(dir ? p.dO : p.v, row0, p.H, h, j0, Lc);
+    const auto fetch = [&](int i) {
+        if (i < nc) {
+            const int c = chunk(i), Lc = min(C, sp.len - c * C);
+            const long long row0 = sp.t0 + (long long)c * C;
+            fetch_tile<Tin, DK, DK>(sA + (i & 1) * C * KP, KP, dir ? p.q : p.k, row0, p.H, h, 0, Lc);
+            fetch_tile<Tin, DV, ROWS>(sB + (i & 1) * C * VP, VP, dir ? p.dO : p.v, row0, p.H, h, j0, Lc);
+        }
+        copies_commit();
+    };
+    const float2 g0 = make_float2(0.f, 0.f);
+    float2 gate = g0, gate_end = g0;  // this thread's row's, and the chunk's
+    const auto load_gate = [&](int i) {
+        if (i >= nc || threadIdx.x >= C) return;
+        const float2 *G = reinterpret_cast<const float2 *>(s.gates + ((size_t)(sp.slot + chunk(i)) * p.H + h) * GATE);
+        gate = __ldg(G + threadIdx.x);
+        gate_end = __ldg(G + C - 1);
     };
     float total = 1.f;
-    if (nc > 0) load(0);
+    fetch(0);
+    load_gate(0);
+    fetch(1);
     for (int i = 0; i < nc; ++i) {
+        float *weight = sW + (i & 1) * (C + 4);  // of the rows; and what is kept of X
+        if (threadIdx.x < C) {
+            weight[threadIdx.x] = dir ? p.scale * hla_decay(gate, g0) : hla_decay(gate_end, gate);
+            if (threadIdx.x == 0) weight[C] = hla_decay(gate_end, g0);
+        }
+        load_gate(i + 1);
+        copies_wait<1>();
+        __syncthreads();
         if (!s.ends) {
             float *dst = s.X[dir] + ((size_t)(sp.slot + chunk(i)) * p.H + h) * (size_t)(DV * DK);
             each([&](size_t at, float &u, float &v) { *reinterpret_cast<float2 *>(dst + at) = make_float2(u, v); });
         }
-        if (threadIdx.x < C) G[threadIdx.x] = gate;
-        ta.store(sA, KP, [&](int) { return 1.f; });
-        __syncthreads();
-        const float2 g0 = make_float2(0.f, 0.f), gC = G[C - 1];
-        tb.store(sB, VP, [&](int r) { return r >= C ? 0.f : dir ? p.scale * hla_decay(G[r], g0) : hla_decay(gC, G[r]); });
-        const float keep = hla_decay(gC, g0);
+        const float keep = weight[C];
         total *= keep;
-        __syncthreads();
-        if (i + 1 < nc) load(i + 1);  // on its way while this one is multiplied
         if (active) {
 #pragma unroll
             for (int a = 0; a < 2; ++a)
@@ -252,9 +264,10 @@ __global__ void __launch_bounds__(NT, 2) hla_state_simt_kernel(const StateArgs s
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[a][j][e] *= keep;
-            mm<C, 8 * WN, true, false>(x, w, sB, VP, sA, KP);
+            mm<C, 8 * WN, true, false, true>(x, w, sB + (i & 1) * C * VP, VP, sA + (i & 1) * C * KP, KP, weight);
         }
         __syncthreads();  // the tiles are consumed
+        fetch(i + 2);
     }
     if (end) each([&](size_t at, float &u, float &v) { *reinterpret_cast<float2 *>(end + at) = make_float2(u, v); });
     if (s.ends && j0 == 0 && threadIdx.x == 0) s.seg.keep[dir][su * p.H + h] = total;
@@ -318,9 +331,11 @@ __global__ void __launch_bounds__(NT, 2) hla_out_simt_kernel(const HlaArgs p, co
     const WarpTile w = tile_of_warp<32>();
     const bool has_state = c > 0 || p.S0 != nullptr;
 
-    load_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc, p.scale);
-    load_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
+    fetch_tile<Tin, DK, DK>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc);
+    fetch_tile<Tin, DK, DK>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
+    copies_commit();
     if (threadIdx.x < C) G[threadIdx.x] = gate_of(gates, slot, p.H, h);
+    copies_wait<0>();
     __syncthreads();
     {
         float a[2][2][4];
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(NT, 2) hla_out_simt_kernel(const HlaArgs p, co
                 for (int e = 0; e < 4; e += 2) {
                     const int r = w.row(i, e), s = w.col<32>(j, e);
                     *reinterpret_cast<float2 *>(sP + r * LP + s) =
-                        make_float2(s <= r ? a[i][j][e] * hla_decay(G[r], G[s]) : 0.f, s + 1 <= r ? a[i][j][e + 1] * hla_decay(G[r], G[s + 1]) : 0.f);
+                        make_float2(s <= r ? a[i][j][e] * (p.scale * hla_decay(G[r], G[s])) : 0.f, s + 1 <= r ? a[i][j][e + 1] * (p.scale * hla_decay(G[r], G[s + 1])) : 0.f);
                 }
     }
     __syncthreads();  // P is written, K's tile is free
@@ -345,10 +360,9 @@ __global__ void __launch_bounds__(NT, 2) hla_out_simt_kernel(const HlaArgs p, co
         constexpr int JT = DV < 64 ? DV : 64;  // rows of the state at a time
 #pragma unroll
         for (int jb = 0; jb < DV / JT; ++jb) {
-            for (int idx = threadIdx.x; idx < JT * (DK / 4); idx += NT) {
-                const int r = idx / (DK / 4), cc = 4 * (idx % (DK / 4));
-                *reinterpret_cast<float4 *>(sK + r * L::KP + cc) = ld4(S + (size_t)(jb * JT + r) * DK + cc);
-            }
+            fetch_state<DK>(sK, L::KP, S + (size_t)jb * JT * DK, JT);
+            copies_commit();
+            copies_wait<0>();
             __syncthreads();
             float part[2][JT / 32][4];
             zero(part);
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(NT, 2) hla_out_simt_kernel(const HlaArgs p, co
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-                const float since = hla_decay(G[w.row(i, e)], make_float2(0.f, 0.f));
+                const float since = p.scale * hla_decay(G[w.row(i, e)], make_float2(0.f, 0.f));
 #pragma unroll
                 for (int j = 0; j < VJ; ++j) {
                     acc[i][j][e] *= since;
@@ -373,7 +387,9 @@ __global__ void __launch_bounds__(NT, 2) hla_out_simt_kernel(const HlaArgs p, co
                 }
             }
     }
-    load_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
+    fetch_tile<Tin, DV, DV>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
+    copies_commit();
+    copies_wait<0>();
     __syncthreads();
     mm<C, 32, false, false>(acc, w, sP, LP, sV, L::VP);
     Tin *o = static_cast<Tin *>(p.o);
@@ -420,30 +436,40 @@ __global__ void __launch_bounds__(NG) hla_grad_simt_kernel(const HlaArgs p, cons
     const WarpTile w = tile_of_warp<16>();
     const float2 g0 = make_float2(0.f, 0.f);
 
-    load_tile<Tin, DK, DK, NG>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc);
-    load_tile<Tin, DK, DK, NG>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
-    load_tile<Tin, DV, DV, NG>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
-    load_tile<Tin, DV, DV, NG>(sO, L::VP, p.dO, row0, p.H, h, 0, Lc, p.scale);
+    // the states' tiles come one ahead, into what the scores take later
+    const size_t xb = ((size_t)slot * p.H + h) * (size_t)(DV * DK);
+    constexpr int JN = DV / JB;
+    const auto states = [&](int jb) {
+        if (jb < JN) {
+            float *to = jb & 1 ? sA : sX;
+            fetch_state<DK, NG>(to, L::KP, Sc + xb + (size_t)jb * JB * DK, JB);
+            fetch_state<DK, NG>(to + JB * L::KP, L::KP, Rc + xb + (size_t)jb * JB * DK, JB);
+        }
+        copies_commit();
+    };
+    fetch_tile<Tin, DK, DK, NG>(sQ, L::KP, p.q, row0, p.H, h, 0, Lc);
+    fetch_tile<Tin, DK, DK, NG>(sK, L::KP, p.k, row0, p.H, h, 0, Lc);
+    fetch_tile<Tin, DV, DV, NG>(sV, L::VP, p.v, row0, p.H, h, 0, Lc);
+    fetch_tile<Tin, DV, DV, NG>(sO, L::VP, p.dO, row0, p.H, h, 0, Lc);
+    states(0);
+    states(1);
     if (threadIdx.x < C) G[threadIdx.x] = gate_of(gates, slot, p.H, h);
-    __syncthreads();
 
     // the parts that go through the states: dQ from S_in, dK and dV from R, and their terms of dg
     float dq[1][KJ][4], dk[1][KJ][4], dv[1][VJ][4];
     zero(dq);
     zero(dk);
     float thr = 0.f;
-    const size_t xb = ((size_t)slot * p.H + h) * (size_t)(DV * DK);
-    float *sS = sX, *sR = sX + JB * L::KP;
 #pragma unroll
-    for (int jb = 0; jb < DV / JB; ++jb) {
+    for (int jb = 0; jb < JN; ++jb) {
+        float *sS = jb & 1 ? sA : sX, *sR = sS + JB * L::KP;
+        copies_wait<1>();
+        __syncthreads();
         for (int idx = threadIdx.x; idx < JB * (DK / 4); idx += NG) {
-            const int r = idx / (DK / 4), cc = 4 * (idx % (DK / 4));
-            const float4 s4 = ld4(Sc + xb + (size_t)(jb * JB + r) * DK + cc), r4 = ld4(Rc + xb + (size_t)(jb * JB + r) * DK + cc);
-            *reinterpret_cast<float4 *>(sS + r * L::KP + cc) = s4;
-            *reinterpret_cast<float4 *>(sR + r * L::KP + cc) = r4;
+            const int at = idx / (DK / 4) * L::KP + 4 * (idx % (DK / 4));
+            const float4 s4 = *reinterpret_cast<const float4 *>(sS + at), r4 = *reinterpret_cast<const float4 *>(sR + at);
             thr = fmaf(s4.x, r4.x, fmaf(s4.y, r4.y, fmaf(s4.z, r4.z, fmaf(s4.w, r4.w, thr))));
         }
-        __syncthreads();
         mm<JB, 32, false, false>(dq, w, sO + jb * JB, L::VP, sS, L::KP);
         mm<JB, 32, false, false>(dk, w, sV + jb * JB, L::VP, sR, L::KP);
         float part[1][1][4];
@@ -454,13 +480,14 @@ __global__ void __launch_bounds__(NG) hla_grad_simt_kernel(const HlaArgs p, cons
 #pragma unroll
             for (int e = 0; e < 4; ++e) dv[i][jb][e] = part[i][0][e];
         __syncthreads();
+        states(jb + 2);
     }
 #pragma unroll
     for (int i = 0; i < 1; ++i)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
             const int r = w.row(i, e);
-            const float since = hla_decay(G[r], g0), until = hla_decay(G[C - 1], G[r]);
+            const float since = p.scale * hla_decay(G[r], g0), until = hla_decay(G[C - 1], G[r]);
             float rd = 0.f, wr = 0.f;
 #pragma unroll
             for (int j = 0; j < KJ; ++j)
@@ -491,7 +518,7 @@ __global__ void __launch_bounds__(NG) hla_grad_simt_kernel(const HlaArgs p, cons
     for (int off = 16; off; off >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, off);
     if (lane == 0) sThr[warp] = thr;
 
-    // A = Q K^T . D, dA = dO' V^T . D, and the pairs within the chunk E = A . dO' V^T below the diagonal
+    // A = scale Q K^T . D, dA = scale dO V^T . D, and the pairs within the chunk E = A . dO V^T below the diagonal
     {
         float a[1][2][4], da[1][2][4];
         zero(a);
@@ -506,9 +533,9 @@ __global__ void __launch_bounds__(NG) hla_grad_simt_kernel(const HlaArgs p, cons
                 for (int e = 0; e < 4; ++e) {
                     const int r = w.row(i, e), s = w.col<32>(j, e);
                     const float d = hla_decay(G[r], G[s]);
-                    const float x = s <= r ? a[i][j][e] * d : 0.f;
+                    const float x = s <= r ? a[i][j][e] * (p.scale * d) : 0.f;
                     sA[r * LP + s] = x;
-                    sD[r * LP + s] = s <= r ? da[i][j][e] * d : 0.f;
+                    sD[r * LP + s] = s <= r ? da[i][j][e] * (p.scale * d) : 0.f;
                     sX[r * LP + s] = s < r ? x * da[i][j][e] : 0.f;
                 }
     }
