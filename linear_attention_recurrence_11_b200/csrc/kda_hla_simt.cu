@@ -10,8 +10,9 @@
 // bits, as lo hi + hi lo + hi hi with fp32 accumulation: what is dropped is below 2^-21 of a product, the order of
 // fp32's own rounding. Measured against FFMA register tiles (4 x 8 per thread), the gradients of 16 heads x 2099
 // tokens take 0.4 of the time: a fragment's element is read from shared memory once for 8 to 32 products. For 2 x 1000
-// tokens, 16 heads of 128: states 34 us, outputs 55, gradients 183 (the tensor pipe busy for 0.28 to 0.48 of it; the
-// rest are the tiles' loads, in one CTA per SM for the gradients, whose tiles take 206 KB).
+// tokens, 16 heads of 128: states 30 us (in two segments), outputs 54, gradients 167 (0.43 of the instructions' rate: a
+// fragment's element costs a load and three operations for every instruction, and a tile's 194 KB arrive before it begins,
+// since one tile fills the SM).
 #include "kda_hla.cuh"
 #include "kda_hla_gate.cuh"
 

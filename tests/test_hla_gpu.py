@@ -328,6 +328,31 @@ def test_captured_and_replayed(K):
     assert torch.equal(S, S2)
 
 
+def test_backward_of_many_heads_captured_and_on_two_streams(K):
+    """More chains than SMs: the last heads' chains and the first heads' gradients run side by side, in a graph and beside
+    another stream's as on their own."""
+    xs = [inputs(1, 700, 90, 64, 64, "bf16", seed=40 + i) for i in range(2)]
+    want = [run_backward(K, x) for x in xs]
+
+    def call(x, **kw):
+        return K.kda_hla_backward(x["q"], x["k"], x["v"], x["g"], x["do"], x["S0"], x["dS_T"], **kw)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(xs[0])
+    for i in (0, 1, 0):
+        for n in ("q", "k", "v", "g", "do", "S0", "dS_T"):
+            xs[0][n].copy_(inputs(1, 700, 90, 64, 64, "bf16", seed=40 + i)[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        got = [call(x, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+
+
 def test_no_tokens(K):
     x = inputs(2, 0, 3, 128, 128, "bf16", seed=20)
     o, S = run_forward(K, x)
