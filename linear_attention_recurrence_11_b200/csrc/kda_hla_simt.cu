@@ -37,6 +37,16 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// Rows of 16 bytes of shared memory, eight (or four times eight) by the lanes' addresses: lane 4 g + t gets word t of the
+// g-th row of each eight.
+__device__ __forceinline__ void ld_rows2(const float *p, float &a, float &b) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"((uint32_t)__cvta_generic_to_shared(p)) : "memory");
+}
+__device__ __forceinline__ void ld_rows4(const float *p, float (&v)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"((uint32_t)__cvta_generic_to_shared(p)) : "memory");
+}
+
 // A warp's part of a product: 16 or 32 rows from m0 on, and of every `step` columns 8 from n0 on. With g = lane / 4 and
 // t = lane % 4, c[i][j] holds rows m0 + 16 i + g (elements 0, 1) and + 8 (2, 3), columns n0 + step j + 2 t and + 1.
 struct WarpTile {
@@ -59,6 +69,8 @@ __device__ __forceinline__ WarpTile tile_of_warp() {
 template <int K, int kStep, bool kAT, bool kBT, bool kW = false, int MI, int NJ>
 __device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, const float *A, int lda, const float *B, int ldb,
                                    const float *weight = nullptr) {
+    static_assert(!kBT || NJ == 1 || NJ % 2 == 0, "column tiles are read in pairs");
+    const int lane = 4 * w.g + w.t;
 #pragma unroll 1
     for (int kb = 0; kb < K; kb += 16) {
         float sum[MI][NJ][4];
@@ -67,19 +79,26 @@ __device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, con
             const int k0 = kb + kk;
             uint32_t ah[MI][4], al[MI][4];
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+            for (int i = 0; i < MI; ++i) {
+                float v[4];
+                if (!kAT) ld_rows4(A + (w.m0 + 16 * i + (lane & 15)) * lda + k0 + 4 * (lane >> 4), v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int m = w.m0 + 16 * i + w.g + 8 * (e & 1), k = k0 + w.t + 4 * (e >> 1);
-                    split_tf32((kW ? weight[k] : 1.f) * (kAT ? A[k * lda + m] : A[m * lda + k]), ah[i][e], al[i][e]);
+                    if (kAT) v[e] = (kW ? weight[k] : 1.f) * A[k * lda + m];
+                    split_tf32(v[e], ah[i][e], al[i][e]);
                 }
+            }
+            float two[4];  // B of this column tile and the next
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 uint32_t bh[2], bl[2];
+                if (kBT && NJ == 1) ld_rows2(B + (w.n0 + (lane & 7)) * ldb + k0 + 4 * ((lane >> 3) & 1), two[0], two[1]);
+                if (kBT && NJ > 1 && j % 2 == 0) ld_rows4(B + (w.n0 + kStep * (j + (lane >> 4)) + (lane & 7)) * ldb + k0 + 4 * ((lane >> 3) & 1), two);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int n = w.n0 + kStep * j + w.g, k = k0 + w.t + 4 * e;
-                    split_tf32(kBT ? B[n * ldb + k] : B[k * ldb + n], bh[e], bl[e]);
+                    split_tf32(kBT ? two[2 * (j & 1) + e] : B[k * ldb + n], bh[e], bl[e]);
                 }
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {

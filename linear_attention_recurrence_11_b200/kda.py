@@ -578,7 +578,8 @@ def kda_kcp_scan(S0, M, Z, *, stream=None):
 
 
 # The single-token calls take the GPU two to four microseconds, so what they spend here counts: one test per tensor
-# (_need only says what is wrong with it), no context manager on the current device, plain integers as pointers.
+# (_need only says what is wrong with it), no context manager on the current device, plain integers as pointers, sizes as
+# arguments of torch.empty (a tuple of them costs it a microsecond more).
 _NO_SIZE = ctypes.c_size_t(-1).value
 _NO_CONTEXT = contextlib.nullcontext()
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -700,7 +701,7 @@ def kda_hla_forward(q, k, v, g, S0=None, *, scale: float = 1.0, cu_seqlens=None,
         if S_T is not None:
             _check(S_T, "S_T", torch.float32, (N, H, dv, dk), dev)
         elif return_state:
-            S_T = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev)
+            S_T = torch.empty(N, H, dv, dk, dtype=torch.float32, device=dev)
         ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_forward")
         rc = _lib.kda_hla_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), o.data_ptr(), _addr(S_T),
                                   B, T, H, dk, dv, scale, dt, gate, _addr(cu_seqlens), packed, ws, ws_bytes,
@@ -729,7 +730,7 @@ def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, 
     with _on(dev, stream):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         dg = torch.empty_like(g) if gate == KDA_HLA_GATE_TOKEN and return_dg else None
-        dS0 = torch.empty((N, H, dv, dk), dtype=torch.float32, device=dev) if return_dS0 else None
+        dS0 = torch.empty(N, H, dv, dk, dtype=torch.float32, device=dev) if return_dS0 else None
         ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_backward")
         rc = _lib.kda_hla_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), do.data_ptr(), _addr(dS_T),
                                    dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), _addr(dg), _addr(dS0), B, T, H, dk, dv,
