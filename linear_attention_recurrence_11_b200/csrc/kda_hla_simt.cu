@@ -10,7 +10,7 @@
 // bits, as lo hi + hi lo + hi hi with fp32 accumulation: what is dropped is below 2^-21 of a product, the order of
 // fp32's own rounding. Measured against FFMA register tiles (4 x 8 per thread), the gradients of 16 heads x 2099
 // tokens take 0.4 of the time: a fragment's element is read from shared memory once for 8 to 32 products. For 2 x 1000
-// tokens, 16 heads of 128: states 30 us (in two segments), outputs 54, gradients 167 (0.43 of the instructions' rate: a
+// tokens, 16 heads of 128: states 30 us (in two segments), outputs 51, gradients 158 (0.45 of the instructions' rate: a
 // fragment's element costs a load and three operations for every instruction, and a tile's 194 KB arrive before it begins,
 // since one tile fills the SM).
 #include "kda_hla.cuh"
@@ -24,7 +24,7 @@ constexpr int NT = 256;
 constexpr int NG = 512;     // of the gradients: one CTA per SM, 4 x 4 warps
 constexpr int JB = 32;      // dv rows of a state tile of the gradients
 constexpr uint32_t GATE = kHlaGateBytes<C>;
-constexpr int LP = C + 4;   // row strides are 4 mod 32 floats: the fragments' reads along rows hit all banks
+constexpr int LP = C + 4;   // row strides are 4 mod 32 floats, but where a comment says otherwise: no bank conflicts along rows
 
 // ------------------------------------------------------------------ products
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
@@ -71,6 +71,11 @@ __device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, con
                                    const float *weight = nullptr) {
     static_assert(!kBT || NJ == 1 || NJ % 2 == 0, "column tiles are read in pairs");
     const int lane = 4 * w.g + w.t;
+    // Which k of the eight is whose does not matter as long as A and B agree. Rows by matrix loads come as t and t + 4;
+    // where both are read down the columns, 2 t and 2 t + 1 spread over all banks if row strides are 4 mod 32 (else 8).
+    constexpr bool kCols = kAT && !kBT;
+    const int kt = kCols ? 2 * w.t : w.t;
+    constexpr int kNext = kCols ? 1 : 4;
 #pragma unroll 1
     for (int kb = 0; kb < K; kb += 16) {
         float sum[MI][NJ][4];
@@ -84,7 +89,7 @@ __device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, con
                 if (!kAT) ld_rows4(A + (w.m0 + 16 * i + (lane & 15)) * lda + k0 + 4 * (lane >> 4), v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int m = w.m0 + 16 * i + w.g + 8 * (e & 1), k = k0 + w.t + 4 * (e >> 1);
+                    const int m = w.m0 + 16 * i + w.g + 8 * (e & 1), k = k0 + kt + kNext * (e >> 1);
                     if (kAT) v[e] = (kW ? weight[k] : 1.f) * A[k * lda + m];
                     split_tf32(v[e], ah[i][e], al[i][e]);
                 }
@@ -97,7 +102,7 @@ __device__ __forceinline__ void mm(float (&c)[MI][NJ][4], const WarpTile &w, con
                 if (kBT && NJ > 1 && j % 2 == 0) ld_rows4(B + (w.n0 + kStep * (j + (lane >> 4)) + (lane & 7)) * ldb + k0 + 4 * ((lane >> 3) & 1), two);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int n = w.n0 + kStep * j + w.g, k = k0 + w.t + 4 * e;
+                    const int n = w.n0 + kStep * j + w.g, k = k0 + kt + kNext * e;
                     split_tf32(kBT ? two[2 * (j & 1) + e] : B[k * ldb + n], bh[e], bl[e]);
                 }
 #pragma unroll
@@ -194,7 +199,7 @@ struct StateArgs {
 template <int DK, int DV>
 struct StateTile {
     static constexpr int ROWS = DV < 64 ? 32 : 64, WN = ROWS == 64 ? 4 : DK < 64 ? 4 : 8, NJ = DK / (8 * WN);
-    static constexpr int KP = DK + 8, VP = ROWS + 8;  // (read down the columns: 8 mod 32)
+    static constexpr int KP = DK + 4, VP = ROWS + 4;
     static constexpr size_t bytes = sizeof(float) * (2 * C * (KP + VP) + 2 * (C + 4));  // two chunks' tiles, weights and decay
 };
 
@@ -428,9 +433,10 @@ __global__ void __launch_bounds__(NT, 2) hla_out_simt_kernel(const HlaArgs p, co
 // ---------------------------------------------------------------- gradients
 template <int DK, int DV>
 struct GradSmem {
-    static constexpr int KP = DK + 4, VP = DV + 4;
-    // the last tile holds the state's tiles (JB x KP each) first, then the pairs of dg
-    static constexpr int XT = (2 * JB * KP > C * LP) ? 2 * JB * KP : C * LP;
+    static constexpr int KP = DK + 4, VP = DV + 4, SP = DK + 8;  // (the states' tiles are read down the columns, beside rows)
+    // the last tile holds the state's tiles (JB x SP each) first, then the pairs of dg; A's and dA's hold the next ones
+    static constexpr int XT = (2 * JB * SP > C * LP) ? 2 * JB * SP : C * LP;
+    static_assert(2 * JB * SP <= 2 * C * LP, "the states' tiles fit into A's and dA's");
     static constexpr int floats = 2 * C * KP + 2 * C * VP + 2 * C * LP + XT + 2 * 4 * C + C + 32;
     static constexpr size_t bytes = sizeof(float) * floats + sizeof(float2) * C;
 };
@@ -462,8 +468,8 @@ __global__ void __launch_bounds__(NG) hla_grad_simt_kernel(const HlaArgs p, cons
     const auto states = [&](int jb) {
         if (jb < JN) {
             float *to = jb & 1 ? sA : sX;
-            fetch_state<DK, NG>(to, L::KP, Sc + xb + (size_t)jb * JB * DK, JB);
-            fetch_state<DK, NG>(to + JB * L::KP, L::KP, Rc + xb + (size_t)jb * JB * DK, JB);
+            fetch_state<DK, NG>(to, L::SP, Sc + xb + (size_t)jb * JB * DK, JB);
+            fetch_state<DK, NG>(to + JB * L::SP, L::SP, Rc + xb + (size_t)jb * JB * DK, JB);
         }
         copies_commit();
     };
@@ -482,19 +488,19 @@ __global__ void __launch_bounds__(NG) hla_grad_simt_kernel(const HlaArgs p, cons
     float thr = 0.f;
 #pragma unroll
     for (int jb = 0; jb < JN; ++jb) {
-        float *sS = jb & 1 ? sA : sX, *sR = sS + JB * L::KP;
+        float *sS = jb & 1 ? sA : sX, *sR = sS + JB * L::SP;
         copies_wait<1>();
         __syncthreads();
         for (int idx = threadIdx.x; idx < JB * (DK / 4); idx += NG) {
-            const int at = idx / (DK / 4) * L::KP + 4 * (idx % (DK / 4));
+            const int at = idx / (DK / 4) * L::SP + 4 * (idx % (DK / 4));
             const float4 s4 = *reinterpret_cast<const float4 *>(sS + at), r4 = *reinterpret_cast<const float4 *>(sR + at);
             thr = fmaf(s4.x, r4.x, fmaf(s4.y, r4.y, fmaf(s4.z, r4.z, fmaf(s4.w, r4.w, thr))));
         }
-        mm<JB, 32, false, false>(dq, w, sO + jb * JB, L::VP, sS, L::KP);
-        mm<JB, 32, false, false>(dk, w, sV + jb * JB, L::VP, sR, L::KP);
+        mm<JB, 32, false, false>(dq, w, sO + jb * JB, L::VP, sS, L::SP);
+        mm<JB, 32, false, false>(dk, w, sV + jb * JB, L::VP, sR, L::SP);
         float part[1][1][4];
         zero(part);
-        mm<DK, 32, false, true>(part, w, sK, L::KP, sR, L::KP);
+        mm<DK, 32, false, true>(part, w, sK, L::KP, sR, L::SP);
 #pragma unroll
         for (int i = 0; i < 1; ++i)
 #pragma unroll
