@@ -107,13 +107,14 @@ struct ChainArgs {
 
 // Outputs: one tile each of a, its hi and lo halves, b, q, the state, and the outputs' staging. States: two of a, whose hi
 // halves replace it, two of lo, so that a chunk is scaled while the one before is multiplied (2.0 us a chunk where one
-// took 2.2), and what else fits: one of b and the state, or two of b.
+// took 2.2), and two of b. The state before chunk i is stored from chunk i - 1's lo, which is free by then.
 template <int DKP, int DVP, int kMode>
 struct ChainSmem {
     static constexpr bool out = kMode == kOut;
     static constexpr uint32_t KT = (DKP / 64) * TILE, VT = (DVP / 64) * TILE;
-    static constexpr int NK = out ? 1 : 2, NV = kMode == kEnds ? 2 : 1;  // buffers of a (and of lo), of b
-    static constexpr uint32_t K = 0, HI = out ? KT : 0u, LO = 2 * KT, V = LO + NK * KT, S = V + NV * VT, Q = S + (kMode == kEnds ? 0 : DKP * DVP * 2);
+    static constexpr int NK = out ? 1 : 2, NV = NK;  // buffers of a (and of lo), of b
+    static constexpr uint32_t K = 0, HI = out ? KT : 0u, LO = 2 * KT, V = LO + NK * KT, S = V + NV * VT, Q = S + (out ? DKP * DVP * 2 : 0);
+    static_assert(DKP * DVP * 2 <= KT, "a state fits into lo");
     static constexpr uint32_t O = Q + (out ? KT : 0u);             // 8 warps x 32 rows of 32 columns
     static constexpr uint32_t G = O + (out ? 16 * KB : 0u), BARS = G + 4 * GATE;  // a ring of four chunks' gates
     static constexpr uint32_t bytes = BARS + 256 + 1024;           // slack for 1024-byte alignment
@@ -135,9 +136,9 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // is a pair, of which a chunk takes one: a phase can only be told from the next, not from the one after.
     constexpr int NK = L::NK, NV = L::NV;
     enum { F_K, F_V = F_K + 2, F_Q = F_V + 2,   // tiles have arrived, by buffer (a's with the gates)
-           D_SCALE = F_Q + 1, D_P = D_SCALE + 2, D_X, D_S, D_O, D_E,  // done: hi + lo (pair); scores; increment read; operand; Q S scaled; outputs read (pair)
+           D_SCALE = F_Q + 2, D_P = D_SCALE + 2, D_X, D_S, D_O, D_E,  // done: hi + lo (pair); scores; increment read; operand; Q S scaled; outputs read (pair)
            C_QK = D_E + 2, C_QS, C_PV, C_X, C_END = C_X + 2,  // products (increment: a pair)
-           R_S = F_Q,                           // kStates: the operand tile has been read by its store
+           R_S = F_Q,                           // kStates: the operand tile has been read by its store (pair)
            NBAR = C_END + 1 };
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + NBAR);
 
@@ -219,6 +220,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int Lc = rows_of(i);
             wait_k(i);
             if (i >= NK) wait_pair(C_X, i - NK);  // hi and lo are read
+            if (kMode == kStates && i > 0) wait_pair(R_S, i - 1);  // and the state that lo held since
             if (Lc < C) {  // b's tile is waited for here only, so first what its buffer's load before was there for
                 if (i >= NV) wait_pair(C_X, i - NV);
                 wait_v(i);
@@ -302,35 +304,30 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (start && r < p.dv && col + e < p.dk) v = *reinterpret_cast<const float4 *>(start + row_off + e);
             x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
         }
-        const auto operand = [&]() {  // X in bf16, as a K-major tile of dv rows
+        const auto operand = [&](uint32_t to) {  // X in bf16, as a K-major tile of dv rows
             if (r < DVP) {
 #pragma unroll
                 for (int q = 0; q < NX / 8; ++q)
-                    *reinterpret_cast<uint4 *>(sm + L::S + (col >> 6) * (DVP * 128) + sw128_offset(r, (col & 63) + 8 * q)) =
+                    *reinterpret_cast<uint4 *>(sm + to + (col >> 6) * (DVP * 128) + sw128_offset(r, (col & 63) + 8 * q)) =
                         make_uint4(pack_bf2(x[8 * q], x[8 * q + 1]), pack_bf2(x[8 * q + 2], x[8 * q + 3]),
                                    pack_bf2(x[8 * q + 4], x[8 * q + 5]), pack_bf2(x[8 * q + 6], x[8 * q + 7]));
             }
         };
         if (kMode == kOut && nc > 0) {
-            operand();
+            operand(L::S);
             done(D_S);
         }
         float total = 1.f;  // decay over the chain
         for (int i = 0; i < nc && ok; ++i) {
             if (kMode == kStates) {
-                if (i > 0) {
-                    if (tid == 256) {
-                        bulk_wait_read_all();
-                        mbar_arrive(bars + R_S);
-                    }
-                    __syncwarp();
-                    if (!wait(R_S, i - 1)) break;
-                }
-                operand();
+                const uint32_t at = L::LO + ((i + 1) & 1) * L::KT;
+                operand(at);
                 done(D_S);
                 if (wait(D_S, i) && tid == 256) {
-                    bulk_store(s.blob[dir] + ((size_t)(sp.slot + chunk(i)) * p.H + h) * blob_bytes(DKP, DVP), sm + L::S, DKP * DVP * 2);
+                    bulk_store(s.blob[dir] + ((size_t)(sp.slot + chunk(i)) * p.H + h) * blob_bytes(DKP, DVP), sm + at, DKP * DVP * 2);
                     bulk_commit();
+                    bulk_wait_read_all();  // (the increment is not there yet)
+                    mbar_arrive(bars + R_S + (i & 1));
                 }
                 __syncwarp();
             }
@@ -367,7 +364,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             done(D_X);
             if (kMode != kOut) continue;
             if (i + 1 < nc) {
-                operand();
+                operand(L::S);
                 done(D_S);
             }
             if (!wait(C_PV, i)) break;
@@ -497,7 +494,6 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     }
                     if (i > 0 && !wait(C_PV, i - 1)) break;  // (and the products before it)
                 }
-                if (kMode == kStates && i > 0 && !wait_pair(C_X, i - 1)) break;
                 mbar_arrive_expect_tx(bars + F_V + vb, L::VT);
                 ++nv;
 #pragma unroll
