@@ -219,7 +219,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int i = 0; i < nc && ok; ++i) {
             const int Lc = rows_of(i);
             wait_k(i);
-            if (i >= NK) wait_pair(C_X, i - NK);  // hi and lo are read
+            if (NK == 1 && i > 0) wait_pair(C_X, i - 1);  // hi and lo are read (of two, since a's tile was asked for)
             if (kMode == kStates && i > 0) wait_pair(R_S, i - 1);  // and the state that lo held since
             if (Lc < C) {  // b's tile is waited for here only, so first what its buffer's load before was there for
                 if (i >= NV) wait_pair(C_X, i - NV);
@@ -234,7 +234,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (tok < Lc) {
                 const float2 gt = G(i)[tok];
                 const float w = dir ? p.scale * hla_decay(gt, g0) : hla_decay(G(i)[C - 1], gt);
-#pragma unroll 1
+#pragma unroll(kMode == kOut ? 1 : 2)
                 for (int q = 0; q < NX / 8; ++q) {
                     const uint32_t off = sw128_offset(tok, 8 * (q0 + q));
                     const uint4 v = *reinterpret_cast<const uint4 *>(ra + off);
