@@ -1080,13 +1080,17 @@ cudaError_t pass_t(const HlaArgs &a, bool back) {
     static HlaSmem smem;
     if ((e = smem.raise(kern, bytes)) != cudaSuccess) return e;
     // Chains that fill the SMs once or more and then some of them once again leave the others without work meanwhile. Of
-    // a dense batch, whose chains are of one length, the heads of that last round are a launch of their own, and the
-    // gradients of the heads before run beside it (96 heads x 8192 tokens, 192 chains on 148 SMs: 658 us against 711, and 650 since the chains are quicker).
+    // a dense batch, whose chains are of one length, the heads of that last wave are a launch of their own, and the
+    // gradients of the heads before run beside it, if those come to nearly whole waves (96 heads x 8192 tokens, 192 chains
+    // on 148 SMs: 658 us against 711, and 650 since the chains are quicker).
     const unsigned sms = (unsigned)device_sm_count();
     const long long chains = (long long)a.N * a.H * dirs;
     int h1 = a.H;
-    if (!a.cu_seqlens && !l.sc && chains > sms && chains % sms) h1 = (int)(chains / sms * sms / (a.N * dirs));
-    if (h1 == 0) h1 = a.H;
+    if (!a.cu_seqlens && !l.sc && chains > sms && chains % sms) {
+        const long long per = (long long)a.N * dirs, first = chains / sms * sms / per * per;  // (whole heads)
+        const auto idle = [&](long long n) { return (n + sms - 1) / sms * sms - n; };
+        if (first > 0 && 2 * idle(first) < idle(chains)) h1 = (int)(first / per);
+    }
     s.next = reinterpret_cast<unsigned *>(ws + l.next);
     s.first = units < sms ? units : sms;
     s.hn = h1;

@@ -95,6 +95,7 @@ SHAPES = [  # B, T, H, dk, dv, dtype, gate, S0
     (1, 90, 2, 32, 32, "bf16", "token", True),
     (1, 150, 80, 64, 64, "bf16", "token", True),     # more chains in the backward pass than SMs, and not twice as many
     (2, 129, 43, 128, 64, "bf16", "token", False),
+    (80, 5, 2, 32, 32, "bf16", "token", True),       # (whole heads of which do not come to whole waves)
 ]
 
 
