@@ -541,8 +541,13 @@ struct TileArgs {
 //   dK = dA^T Q + e^{G_C - G_r} V R       T3
 //   dV = A^T dO + e^{G_C - G_r} K R^T     T1 (dP's, once that is read)
 // The product with the state comes first; the threads scale its rows in TMEM, and the other product accumulates on
-// top. A and dA go over S and V, which are free by then. dg comes from row sums in fp32 (below): of terms within the
-// chunk that partly cancel, so it carries about 1e-6 of a token's own terms.
+// top. A and dA go over S and V, which are free by then. dg_t is a sum over pairs of a write before t and a read from t
+// on, and of nothing else (an earlier form took all of q . dQ less all of k . dK, whose pairs on one side of t cancel but for
+// their roundings: from g = -10 down those were larger than what was left). The pairs within the chunk E = A . dP, in fp32,
+// are summed where the scores are masked, a warp's 32 x 32 block to its rows' and columns' sums; the reads of S (rows of
+// q . dQ2) and what R sees of the writes (k . dK2) while those products are scaled.
+// (The pairs' sums take 10 us of 687 for 96 heads x 8192 tokens; held back until the products of dQ and dK run, whose time
+// they would share, they cost spills and 70 us.)
 // Measured for d = 128: 9.4 us a tile, 96 heads x 8192 tokens 393 us (4.6 TB/s of its 288 KB a tile; 6.6 us at the rate
 // of a copy). The phases of a tile follow each other; warps of their own for copies, products and results took longer.
 template <int DKP, int DVP>
@@ -553,11 +558,29 @@ struct GradTile {
     static constexpr uint32_t A = over ? S : R + SB, dA = over ? V : A + 2 * TILE, END = over ? R + SB : dA + 2 * TILE;
     // the results' staging: where nothing is read any more by then, and not over q and k, whose next tiles come first
     static constexpr uint32_t stQ = over ? R : S, stK = dA, stV = A;
-    static constexpr uint32_t G = END + 128, RED = G + 2 * GATE;   // RED: 3 x 4 x 128 floats, and 16
-    static constexpr uint32_t bytes = RED + 12 * C * 4 + 64 + 1024;
+    static constexpr uint32_t G = END + 128, RED = G + 2 * GATE;
+    // RED, in floats: per column warp the reads and the writes of each token; sums of the pairs E over blocks of 32 x 32
+    // below the diagonal, of a row ([column block][row]) and of a column ([row block - 1][column]); in the blocks on the
+    // diagonal the pairs across each token; and each warp's part of <S, R>
+    static constexpr int READS = 0, WRITES = 4 * C, ROWS = 8 * C, COLS = 11 * C, DIAG = 14 * C, THR = 15 * C;
+    static constexpr uint32_t bytes = RED + (THR + 16) * 4 + 1024;
     static_assert(bytes <= 232448, "shared memory budget");
     static_assert(over || QB <= 2 * SB, "dQ is staged over S and R");
 };
+
+// Sums over a warp's lanes of 16 values each: lane l gets that of value l / 2.
+__device__ __forceinline__ float lane_sums(float (&x)[16], int lane) {
+#pragma unroll
+    for (int n = 8; n >= 1; n >>= 1) {  // the lanes of either half keep half of the values
+        const bool upper = lane & (2 * n);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i + n], 2 * n);
+            x[i] = (upper ? x[i + n] : x[i]) + other;
+        }
+    }
+    return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+}
 
 template <int DKP, int DVP>
 __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -759,6 +782,7 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         wait(L_QK);  // (the gates came with q and k)
         wait(B_P);
         wait(B_DP);
+        ok = __all_sync(0xffffffffu, ok);  // (the warp's lanes exchange sums)
         tc_fence_after();
         const float2 gr = G[r];
         const DecayRow dr{G, reinterpret_cast<const float *>(G + C), gr, r, 32 * quarter, Lc, p.scale};
@@ -766,6 +790,8 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 16; ++e) wa[e] = wd[e] = 0u;
         } else if (ok) {
+            const bool diagonal = grp == quarter;
+            float across = 0.f;  // of this row, the pairs with the columns so far
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 float a[16], d[16], f[16];
@@ -779,7 +805,29 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
                     wa[8 * q + e] = pack_bf2(dr.keep(c, a[2 * e], f[2 * e]), dr.keep(c + 1, a[2 * e + 1], f[2 * e + 1]));
                     wd[8 * q + e] = pack_bf2(dr.keep(c, d[2 * e], f[2 * e]), dr.keep(c + 1, d[2 * e + 1], f[2 * e + 1]));
                 }
+                if (p.dg) {
+                    // over the rows: a column's pairs, or (diagonal) those of rows from a token on with columns before it.
+                    // (Rows behind the end are zero on both sides of both products.)
+                    if (diagonal) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int c = col + 16 * q + e;
+                            const float pair = a[e] * f[e] * d[e];
+                            a[e] = c <= r ? across : 0.f;
+                            across += c < r ? pair : 0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            a[e] = a[e] * f[e] * d[e];
+                            across += a[e];
+                        }
+                    }
+                    const float x = lane_sums(a, lane);
+                    if (!(lane & 1)) red[(diagonal ? L::DIAG : L::COLS + (quarter - 1) * C) + col + 16 * q + (lane >> 1)] = x;
+                }
             }
+            if (p.dg && !diagonal) red[L::ROWS + grp * C + r] = across;
         }
         wait(B_SR);  // the products have read S and V ..
         __syncthreads();  // .. and every thread its part of S
@@ -794,9 +842,9 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        // the state's products scaled per row in TMEM; sums of k . dK2 on the way
+        // the state's products scaled per row in TMEM; sums of q . dQ2 and k . dK2 on the way
         const float since = p.scale * hla_decay(gr, g0), until = hla_decay(G[C - 1], gr);
-        float cs2 = 0.f, cs = 0.f, rs = 0.f;
+        float reads = 0.f, writes = 0.f;
         const auto dot16 = [&](uint32_t tile, int cl, const float *v) {
             float x = 0.f;
 #pragma unroll
@@ -820,7 +868,8 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
             for (int e = 0; e < 32; ++e) v[e] *= f;
             tmem_st16(tmem + tlane + T + col, *reinterpret_cast<float(*)[16]>(v));
             tmem_st16(tmem + tlane + T + col + 16u, *reinterpret_cast<float(*)[16]>(v + 16));
-            if (T == T3 && p.dg) cs2 = dot16(L::K, col, v) + dot16(L::K, col + 16, v + 16);
+            if (T == T2 && p.dg) reads = dot16(L::Q, col, v) + dot16(L::Q, col + 16, v + 16);
+            if (T == T3 && p.dg) writes = dot16(L::K, col, v) + dot16(L::K, col + 16, v + 16);
             tmem_wait_st();
         };
         bad = __syncthreads_or(!ok);
@@ -856,10 +905,9 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         }
         __syncwarp();
         // results: staged and written by tensor stores; rows of a partial chunk directly
-        const auto result = [&](uint32_t T, uint32_t stage, void *out, int d, uint32_t dots, float *sum) {
+        const auto result = [&](uint32_t T, uint32_t stage, void *out, int d) {
             float v[32];
             load32(T, v);
-            if (sum && p.dg) *sum = dot16(dots, col, v) + dot16(dots, col + 16, v + 16);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint4 w = make_uint4(pack_bf2(v[8 * q], v[8 * q + 1]), pack_bf2(v[8 * q + 2], v[8 * q + 3]),
@@ -874,16 +922,15 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         wait(B_QK);
         tc_fence_after();
         if (ok && col < DKP) {
-            result(T2, L::stQ, p.dq, p.dk, L::Q, &rs);
-            result(T3, L::stK, p.dk_, p.dk, L::K, &cs);
+            result(T2, L::stQ, p.dq, p.dk);
+            result(T3, L::stK, p.dk_, p.dk);
         }
         if (p.dg) {
-            red[grp * C + r] = rs;
-            red[(4 + grp) * C + r] = cs;
-            red[(8 + grp) * C + r] = cs2;
+            red[L::READS + grp * C + r] = reads;
+            red[L::WRITES + grp * C + r] = writes;
 #pragma unroll
             for (int off = 16; off; off >>= 1) thr += __shfl_xor_sync(0xffffffffu, thr, off);
-            if (lane == 0) red[12 * C + warp] = thr;
+            if (lane == 0) red[L::THR + warp] = thr;
         }
         fence_proxy_async_smem();
         bad = __syncthreads_or(!ok);
@@ -900,45 +947,72 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
             if (more) load_qk(nxt, it + 1);
         }
         __syncwarp();
-        // dg by one warp: what a token from t on reads of one before t. Within the chunk: the later rows' sums
-        // q . dQ less the later columns' sums k . dK1 (pairs that both count, the diagonal among them, cancel; the
-        // rows' sums hold the reads of S too); the earlier columns' k . dK2; and e^{G_C} <S, R>.
         if (tid == 64) s_tile[ph ^ 1] = settle(after);  // (read behind the tile's last barrier)
+        // dg by one warp, four tokens a lane: from t on, the reads of S, and the pairs with the column blocks before t's;
+        // the pairs across t in the diagonal block; before t, the writes that R sees, and the pairs of t's column block with
+        // the row blocks behind; and e^{G_C} <S, R>. Exclusive sums are shifted, not subtracted.
         if (p.dg && warp == 2) {
-            double a[4], b[4];  // (larger terms cancel: fp64, of a few hundred numbers)
+            const int block = lane >> 3;
+            const auto four = [&](int at, float (&x)[4]) {
+                const float4 y = *reinterpret_cast<const float4 *>(red + at + 4 * lane);
+                x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
+            };
+            float from[4][4] = {}, before[2][4] = {}, dg[4] = {};  // sums over the tokens from t on, and before t
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                four(L::READS + k * C, from[0]);
+                four(L::WRITES + k * C, before[0]);
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (block > k) four(L::ROWS + k * C, from[1 + k]);
+                if (block <= k) four(L::COLS + k * C, before[1]);
+            }
+            four(L::DIAG, dg);
+            float through = 0.f;
+            for (int w = 0; w < 16; ++w) through += red[L::THR + w];
+            through *= hla_decay(G[C - 1], g0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float *x = from[k];
+                x[2] += x[3]; x[1] += x[2]; x[0] += x[1];
+                float sum = x[0];
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float y = __shfl_down_sync(0xffffffffu, sum, off);
+                    if (lane + off < 32) sum += y;
+                }
+                sum = __shfl_down_sync(0xffffffffu, sum, 1);
+                if (k == 0 || block >= k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dg[e] += lane < 31 ? x[e] + sum : x[e];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int first = k ? lane & 24 : 0;  // (columns: of this block)
+                const float *x = before[k];
+                const float x1 = x[0] + x[1], x2 = x1 + x[2];
+                float sum = x2 + x[3];
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, sum, off);
+                    if (lane - off >= first) sum += y;
+                }
+                sum = __shfl_up_sync(0xffffffffu, sum, 1);
+                if (lane == first) sum = 0.f;
+                dg[0] += sum; dg[1] += sum + x[0]; dg[2] += sum + x1; dg[3] += sum + x2;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 4 * lane + e;
-                double x[3];
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    x[k] = ((double)red[(4 * k) * C + i] + (double)red[(4 * k + 1) * C + i]) + ((double)red[(4 * k + 2) * C + i] + (double)red[(4 * k + 3) * C + i]);
-                a[e] = x[0] - (x[1] - x[2]);
-                b[e] = x[2];
-            }
-            double after = (a[0] + a[1]) + (a[2] + a[3]), before = (b[0] + b[1]) + (b[2] + b[3]), fb = before, through = 0.0;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const double x = __shfl_down_sync(0xffffffffu, after, off), y = __shfl_up_sync(0xffffffffu, before, off);
-                if (lane + off < 32) after += x;
-                if (lane >= off) before += y;
-            }
-            fb = before - fb;
-            for (int w = 0; w < 16; ++w) through += (double)red[12 * C + w];
-            through *= (double)hla_decay(G[C - 1], g0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 4 * lane + e;
-                if (i < Lc) st_elem(static_cast<__nv_bfloat16 *>(p.dg), (size_t)(cur.row0 + i) * p.H + cur.h, (float)(after + fb + through));
-                after -= a[e];
-                fb += b[e];
+                if (i < Lc) st_elem(static_cast<__nv_bfloat16 *>(p.dg), (size_t)(cur.row0 + i) * p.H + cur.h, dg[e] + through);
             }
         }
         wait(B_V);
         tc_fence_after();
         if (copier && ok && more) load_o(nxt);
         __syncwarp();
-        if (ok && col < DVP) result(T1, L::stV, p.dv_, p.dv, 0, nullptr);
+        if (ok && col < DVP) result(T1, L::stV, p.dv_, p.dv);
         fence_proxy_async_smem();
         tc_fence_before();
         bad = __syncthreads_or(!ok);
