@@ -453,7 +453,10 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
  * for every (sequence, head), with a scalar log-decay g_t. Layouts, states,
  * packed batches, ownership, alignment and errors as above (q, k [B, T, H, dk],
  * v, o [B, T, H, dv], states fp32 [N, H, dv, dk]); there is no beta, k and q
- * need no normalisation, and nothing bounds g from below.
+ * need no normalisation, and nothing bounds g from below. What is read by
+ * element need only be aligned as its elements are: cu_seqlens, g of
+ * kda_hla_decode_step, positions and inv_freq of kda_rope; and q, k and the
+ * outputs of kda_rope may begin wherever a row of an aligned tensor may.
  *
  *   gate   : KDA_HLA_GATE_TOKEN: g [B, T, H] of type dtype, one log-decay per
  *            token and head; KDA_HLA_GATE_HEAD: g fp32 [H], the same for every

@@ -6,7 +6,9 @@
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned16(const void *p) { return aligned(p, 16); }
+size_t dtype_bytes(int t) { return t == KDA_DTYPE_F32 ? 4 : 2; }
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool dtype_ok(int t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_BF16; }
 bool gate_ok(int g) { return g == KDA_HLA_GATE_TOKEN || g == KDA_HLA_GATE_HEAD; }
@@ -63,9 +65,10 @@ int kda_hla_forward(const void *q, const void *k, const void *v, const void *g, 
     if (st) return st;
     if (!gate_ok(gate)) return KDA_ERR_INVALID_ARG;
     if (T > 0 && (!q || !k || !v || !g || !o)) return KDA_ERR_INVALID_ARG;
-    for (const void *p : {q, k, v, g, (const void *)S0, (const void *)o, (const void *)S_T, (const void *)cu_seqlens,
+    for (const void *p : {q, k, v, g, (const void *)S0, (const void *)o, (const void *)S_T,
                           (const void *)workspace, (const void *)dev_status})
         if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(cu_seqlens, sizeof(int32_t))) return KDA_ERR_ALIGNMENT;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.o = o; a.ST = S_T;
     a.scale = scale; a.gate = gate; a.cu_seqlens = cu_seqlens;
     a.workspace = workspace; a.workspace_bytes = workspace_bytes; a.dev_status = dev_status;
@@ -86,9 +89,10 @@ int kda_hla_backward(const void *q, const void *k, const void *v, const void *g,
     if (gate == KDA_HLA_GATE_HEAD && dg) return KDA_ERR_INVALID_ARG;  // a head's fixed decay has no gradient
     if (T > 0 && (!q || !k || !v || !g || !dO || !dq || !dk_out || !dv_out)) return KDA_ERR_INVALID_ARG;
     for (const void *p : {q, k, v, g, (const void *)S0, dO, (const void *)dS_T, (const void *)dq, (const void *)dk_out,
-                          (const void *)dv_out, (const void *)dg, (const void *)dS0, (const void *)cu_seqlens,
+                          (const void *)dv_out, (const void *)dg, (const void *)dS0,
                           (const void *)workspace, (const void *)dev_status})
         if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(cu_seqlens, sizeof(int32_t))) return KDA_ERR_ALIGNMENT;
     a.q = q; a.k = k; a.v = v; a.g = g; a.S0 = S0; a.dO = dO; a.dST = dS_T;
     a.dq = dq; a.dk_ = dk_out; a.dv_ = dv_out; a.dg = dg; a.dS0 = dS0;
     a.scale = scale; a.gate = gate; a.cu_seqlens = cu_seqlens;
@@ -109,8 +113,9 @@ int kda_hla_decode_step(const void *q, const void *k, const void *v, const void 
     if (!head_dim_ok(dk) || !head_dim_ok(dv)) return KDA_ERR_UNSUPPORTED;
     if ((long long)N * H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     if (!q || !k || !v || !g || !S || !o) return KDA_ERR_INVALID_ARG;
-    for (const void *p : {q, k, v, g, (const void *)S, (const void *)o})
+    for (const void *p : {q, k, v, (const void *)S, (const void *)o})
         if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(g, gate == KDA_HLA_GATE_HEAD ? sizeof(float) : dtype_bytes(dtype))) return KDA_ERR_ALIGNMENT;
     const kda::HlaDecodeArgs a{q, k, v, g, S, o, N, H, dk, dv, dtype, gate, scale, static_cast<cudaStream_t>(stream)};
     return kda::cuda_status(kda::launch_hla_decode(a));
 }
@@ -126,8 +131,11 @@ int kda_rope(const void *q, const void *k, const void *positions, int positions_
         if (T > 0 || Hk == 0) return KDA_ERR_INVALID_ARG;
     }
     if (T > 0 && (!q || !q_out || !inv_freq)) return KDA_ERR_INVALID_ARG;
-    for (const void *p : {q, k, positions, (const void *)inv_freq, (const void *)q_out, (const void *)k_out})
-        if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
+    // rows of 16-byte pieces, or of the widest that a row divides into
+    const size_t row = d * dtype_bytes(dtype), piece = row % 16 == 0 ? 16 : row % 8 == 0 ? 8 : 4;
+    for (const void *p : {q, k, (const void *)q_out, (const void *)k_out})
+        if (!aligned(p, piece)) return KDA_ERR_ALIGNMENT;
+    if (!aligned(positions, positions_64bit ? sizeof(int64_t) : sizeof(int32_t)) || !aligned(inv_freq, sizeof(float))) return KDA_ERR_ALIGNMENT;
     kda::RopeArgs a{};
     a.q = q; a.k = k; a.positions = positions; a.inv_freq = inv_freq; a.q_out = q_out; a.k_out = k_out;
     a.tokens = (long long)B * T; a.T = T; a.Hq = Hq; a.Hk = Hk; a.d = d; a.rot_dim = rot_dim;

@@ -609,6 +609,11 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _aligned(t):
+    """t, or a copy (made on the current stream) if it begins between 16-byte boundaries, as a view of some tokens may."""
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 def _hla_gate(g, dtype, shape, dev):
     """KDA_HLA_GATE_*: g of the activations' type, one number per token and head, or fp32 ``[H]``."""
     if isinstance(g, torch.Tensor) and g.dim() == 1:
@@ -703,6 +708,7 @@ def kda_hla_forward(q, k, v, g, S0=None, *, scale: float = 1.0, cu_seqlens=None,
         elif return_state:
             S_T = torch.empty(N, H, dv, dk, dtype=torch.float32, device=dev)
         ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_forward")
+        g = _aligned(g)
         rc = _lib.kda_hla_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), o.data_ptr(), _addr(S_T),
                                   B, T, H, dk, dv, scale, dt, gate, _addr(cu_seqlens), packed, ws, ws_bytes,
                                   _addr(dev_status), _raw_stream(stream, dev), way)
@@ -732,6 +738,7 @@ def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, 
         dg = torch.empty_like(g) if gate == KDA_HLA_GATE_TOKEN and return_dg else None
         dS0 = torch.empty(N, H, dv, dk, dtype=torch.float32, device=dev) if return_dS0 else None
         ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_backward")
+        g = _aligned(g)
         rc = _lib.kda_hla_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), do.data_ptr(), _addr(dS_T),
                                    dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), _addr(dg), _addr(dS0), B, T, H, dk, dv,
                                    scale, dt, gate, _addr(cu_seqlens), packed, ws, ws_bytes, _addr(dev_status),
