@@ -48,17 +48,23 @@ constexpr uint32_t GATE = kHlaGateBytes<C>;
 // x D_rs, D_rs = 2^{G_r - G_s} for s <= r, and 0 above. Columns that all come before these rows take D_rs as
 // 2^{G_r - G_e} F_s, e the last of the 32 columns: both factors are at most 1, the second is the same for all rows, and
 // a product replaces the exponential (5 instructions an element instead of 12). On the diagonal the first factor is
-// 1 or more; it and F_s keep their precision as long as these 32 tokens together decay by less than 2^-60.
+// 1 or more; it and F_s keep their precision as long as no sum of these 32 tokens is more than 60 away from the last one's
+// (either way: a positive g grows).
 struct DecayRow {
     const float2 *G;
     const float *F;
     float2 gr;
     int r, R, Lc;
     float scale;
+    bool mild;  // the sums of the 32 rows are near each other
+    // (by the warp of rows R ..)
+    __device__ __forceinline__ DecayRow(const float2 *gates, int row, int rows, float s)
+        : G(gates), F(reinterpret_cast<const float *>(gates + C)), gr(gates[row]), r(row), R(row & ~31), Lc(rows), scale(s),
+          mild(__all_sync(0xffffffffu, fabsf(gr.x - gates[row | 31].x) <= 60.f)) {}
     // the decays of 16 columns, times scale; zero where masked
     __device__ __forceinline__ bool none(int col) const { return col > R + 31; }
     __device__ __forceinline__ void get(int col, float (&d)[16]) const {
-        if (col < R || G[col & ~31].x - G[col | 31].x <= 60.f) {
+        if (col < R || mild) {
             const float x = r < Lc ? scale * hla_decay(gr, G[col | 31]) : 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
@@ -268,7 +274,7 @@ hla_chain_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (kMode != kOut) continue;
             if (!wait(C_QK, i)) break;
             tc_fence_after();
-            const DecayRow dr{G(i), reinterpret_cast<const float *>(G(i) + C), G(i)[r], r, R, Lc, p.scale};
+            const DecayRow dr(G(i), r, Lc, p.scale);
             // (a loop of 16 columns, not unrolled: the warps' roles are long straight lines of code, and what is not
             // fetched again runs at a third of the rate)
 #pragma unroll 1
@@ -785,7 +791,7 @@ __global__ void __launch_bounds__(512, 1) hla_grad_tc_kernel(const __grid_consta
         ok = __all_sync(0xffffffffu, ok);  // (the warp's lanes exchange sums)
         tc_fence_after();
         const float2 gr = G[r];
-        const DecayRow dr{G, reinterpret_cast<const float *>(G + C), gr, r, 32 * quarter, Lc, p.scale};
+        const DecayRow dr(G, r, Lc, p.scale);
         if (dr.none(col)) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) wa[e] = wd[e] = 0u;
