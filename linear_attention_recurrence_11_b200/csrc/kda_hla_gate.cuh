@@ -31,14 +31,15 @@ __global__ void __launch_bounds__(256) hla_gate_kernel(const HlaArgs p, uint8_t 
     __shared__ long long tot[SEGS][32];
     __shared__ int nans[SEGS][32];
     __shared__ float2 sG[C * LG];  // [token][head]
-    const long long slot = blockIdx.x;
+    const int groups = (p.H + 31) / 32, h0 = (int)(blockIdx.x % groups) * 32;  // (one axis: the second ends at 65535 blocks)
+    const long long slot = blockIdx.x / groups;
     const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5;
     int n, c;
     HlaSpan sp;
     if (!hla_chunk_of(p, slot, C, n, c, sp)) return;
     const int Lc = min(C, sp.len - c * C);
     const size_t row0 = (size_t)(sp.t0 + (long long)c * C);
-    const int hh = min((int)(blockIdx.y * 32) + lane, p.H - 1);
+    const int hh = min(h0 + lane, p.H - 1);
     float g[E];
     if (p.gate == KDA_HLA_GATE_HEAD) {
         const float x = static_cast<const float *>(p.g)[hh];
@@ -78,8 +79,8 @@ __global__ void __launch_bounds__(256) hla_gate_kernel(const HlaArgs p, uint8_t 
     }
     __syncthreads();
     // out by heads, a warp each: 256 and 128 contiguous bytes at a time
-    for (int i = seg; i < 32 && blockIdx.y * 32 + i < p.H; i += SEGS) {
-        uint8_t *dst = gates + ((size_t)slot * p.H + blockIdx.y * 32 + i) * kHlaGateBytes<C>;
+    for (int i = seg; i < 32 && h0 + i < p.H; i += SEGS) {
+        uint8_t *dst = gates + ((size_t)slot * p.H + h0 + i) * kHlaGateBytes<C>;
 #pragma unroll
         for (int k = 0; k < C / 32; ++k) {
             const int s = 32 * k + lane;
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(256) hla_gate_kernel(const HlaArgs p, uint8_t 
 
 template <typename Tin, int C>
 cudaError_t launch_hla_gates(const HlaArgs &a, long long slots, uint8_t *gates) {
-    hla_gate_kernel<Tin, C><<<dim3((unsigned)slots, (a.H + 31) / 32), 256, 0, a.stream>>>(a, gates);
+    hla_gate_kernel<Tin, C><<<(unsigned)(slots * ((a.H + 31) / 32)), 256, 0, a.stream>>>(a, gates);
     return cudaGetLastError();
 }
 

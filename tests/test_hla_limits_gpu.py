@@ -42,3 +42,20 @@ def test_rows_before_an_overflow(K, dtype):
     o64, _ = forward64(x, 0.125)
     for t in range(27):
         assert rel(o[:, t], o64[:, t]) < 4 * TOL[dtype], t
+
+
+def test_more_heads_than_a_grids_second_axis(K):
+    """More than 65535 x 32 heads: prefill in bf16, backward pass in fp32."""
+    H, d = 65535 * 32 + 33, 32
+    gen = torch.Generator(device="cuda").manual_seed(73)
+    q, k, v, do = (torch.randn(1, 1, H, d, generator=gen, device="cuda") for _ in range(4))
+    g = -torch.rand(1, 1, H, generator=gen, device="cuda")
+    low = [y.bfloat16() for y in (q, k, v, g)]
+    o, _ = K.kda_hla_forward(*low, return_state=False)
+    a, b, c = (y.double() for y in low[:3])
+    # the score, q k^T, is rounded to bf16 and so is the result
+    assert rel(o, (a * b).sum(-1, keepdim=True) * c) < 2 * 2.0 ** -8
+    dq, dk, dv, dg, _ = K.kda_hla_backward(q, k, v, g, do, return_dS0=False)
+    s, w = (do.double() * v.double()).sum(-1, keepdim=True), (q.double() * k.double()).sum(-1, keepdim=True)
+    assert rel(dq, s * k.double()) < 1e-5 and rel(dk, s * q.double()) < 1e-5 and rel(dv, w * do.double()) < 1e-5
+    assert (dg == 0).all()
