@@ -655,12 +655,10 @@ _hla_forward_size = functools.lru_cache(maxsize=4096)(_lib.kda_hla_forward_works
 _hla_backward_size = functools.lru_cache(maxsize=4096)(_lib.kda_hla_backward_workspace_size)
 
 
-def _hla_workspace(size, workspace, dev, where):
+def _hla_workspace(size, workspace, dev):
     """Address and bytes of the workspace, and what keeps it alive."""
-    if size == _NO_SIZE:
-        raise KdaError(KDA_ERR_UNSUPPORTED, where)
     if workspace is None:
-        if not size:
+        if not size or size == _NO_SIZE:  # (sizes without a workspace are refused by the call, which knows why)
             return None, 0, None
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         return workspace.data_ptr(), size, workspace
@@ -707,7 +705,7 @@ def kda_hla_forward(q, k, v, g, S0=None, *, scale: float = 1.0, cu_seqlens=None,
             _check(S_T, "S_T", torch.float32, (N, H, dv, dk), dev)
         elif return_state:
             S_T = torch.empty(N, H, dv, dk, dtype=torch.float32, device=dev)
-        ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_forward")
+        ws, ws_bytes, held = _hla_workspace(size, workspace, dev)
         g = _aligned(g)
         rc = _lib.kda_hla_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), o.data_ptr(), _addr(S_T),
                                   B, T, H, dk, dv, scale, dt, gate, _addr(cu_seqlens), packed, ws, ws_bytes,
@@ -737,7 +735,7 @@ def kda_hla_backward(q, k, v, g, do, S0=None, dS_T=None, *, scale: float = 1.0, 
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         dg = torch.empty_like(g) if gate == KDA_HLA_GATE_TOKEN and return_dg else None
         dS0 = torch.empty(N, H, dv, dk, dtype=torch.float32, device=dev) if return_dS0 else None
-        ws, ws_bytes, held = _hla_workspace(size, workspace, dev, "kda_hla_backward")
+        ws, ws_bytes, held = _hla_workspace(size, workspace, dev)
         g = _aligned(g)
         rc = _lib.kda_hla_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(S0), do.data_ptr(), _addr(dS_T),
                                    dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), _addr(dg), _addr(dS0), B, T, H, dk, dv,

@@ -59,3 +59,20 @@ def test_more_heads_than_a_grids_second_axis(K):
     s, w = (do.double() * v.double()).sum(-1, keepdim=True), (q.double() * k.double()).sum(-1, keepdim=True)
     assert rel(dq, s * k.double()) < 1e-5 and rel(dk, s * q.double()) < 1e-5 and rel(dv, w * do.double()) < 1e-5
     assert (dg == 0).all()
+
+
+def test_codes_of_refusals(K):
+    x = inputs(1, 8, 2, 32, 32, "f32", seed=74)
+    args = [x[n] for n in ("q", "k", "v", "g")]
+
+    def code(f, *a, **kw):
+        with pytest.raises(K.KdaError) as e:
+            f(*a, **kw)
+        return e.value.code
+
+    empty = [y[:0] for y in args]
+    for path, want in (("tc_single", K.KDA_ERR_INVALID_ARG), ("tc", K.KDA_ERR_UNSUPPORTED)):
+        assert code(K.kda_hla_forward, *args, path=path) == want
+        assert code(K.kda_hla_backward, *args, x["do"], path=path) == want
+    assert code(K.kda_hla_forward, *empty) == K.KDA_ERR_INVALID_ARG
+    assert code(K.kda_hla_backward, *empty, x["do"][:0]) == K.KDA_ERR_INVALID_ARG
