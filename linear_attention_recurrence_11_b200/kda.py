@@ -822,6 +822,8 @@ def kda_rope(q, k, inv_freq, *, positions=None, interleaved: bool = False, mscal
     if q.dim() != 4:
         raise ValueError("q is [B, T, H, d]")
     B, T, Hq, d = q.shape
+    if B > 0x7fffffff or T > 0x7fffffff:  # (more than the library's integers hold)
+        raise KdaError(KDA_ERR_UNSUPPORTED, "kda_rope")
     Hk = 0
     if k is not None:
         _need(k, "k", dtype, None, dev)
