@@ -469,7 +469,8 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
  *   cu_seqlens : device int32 [num_seqs + 1] (B must be 1, T is the total) or
  *            NULL (num_seqs is then ignored). Tokens before the first or
  *            behind the last sequence are neither read nor written. Offsets
- *            are clamped to [0, T].
+ *            are clamped to [0, T]. Documented, not checked: they do not
+ *            fall (results are undefined, within the tensors, where they do).
  *   workspace : the states at the chunks' borders; kda_hla_*_workspace_size
  *            (num_seqs 0: a dense batch) gives the bytes, (size_t)-1 for sizes
  *            that the call would refuse. One workspace serves one call at a

@@ -79,7 +79,9 @@ struct HlaSpan {
     long long slot;  // slot of chunk 0
 };
 
-// The offsets are clamped to [0, T] and to increasing order, so that no offset reaches past a tensor.
+// The offsets are clamped to [0, T], and a sequence that would end before it begins is empty, so that whatever they are every
+// row and slot stays inside. Offsets that fall over several sequences can give a row, or a slot, to two of them: then it is
+// undefined which one's result it holds.
 __device__ __forceinline__ HlaSpan hla_span(const HlaArgs &p, int n, int C) {
     HlaSpan s;
     if (p.cu_seqlens) {

@@ -76,3 +76,38 @@ def test_codes_of_refusals(K):
         assert code(K.kda_hla_backward, *args, x["do"], path=path) == want
     assert code(K.kda_hla_forward, *empty) == K.KDA_ERR_INVALID_ARG
     assert code(K.kda_hla_backward, *empty, x["do"][:0]) == K.KDA_ERR_INVALID_ARG
+
+
+GUARD = 4096
+
+
+def guarded(shape, dtype):
+    """A tensor between two runs of bytes of 0x5a."""
+    n = torch.empty(0, dtype=dtype).element_size()
+    for s in shape:
+        n *= s
+    whole = torch.full((n + 2 * GUARD,), 0x5a, dtype=torch.uint8, device="cuda")
+    return whole, whole[GUARD:GUARD + n].view(dtype).view(shape)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cu,clamped", [([0, 50, 1000, 2000], [0, 50, 300, 300]), ([-7, 3, 3, 300], [0, 3, 3, 300]), ([-9, -5, 120, 1 << 30], [0, 0, 120, 300])])
+def test_offsets_past_the_tensors(K, dtype, cu, clamped):
+    """Offsets below zero or past the tokens count as zero and as the number of tokens, and nothing outside the outputs and
+    the workspace is written."""
+    x = inputs(1, 300, 2, 64, 64, dtype, seed=75, N=3)
+    dt = x["v"].dtype
+    c, c2 = (torch.tensor(y, dtype=torch.int32, device="cuda") for y in (cu, clamped))
+    keep_o, o = guarded((1, 300, 2, 64), dt)
+    keep_s, S = guarded((3, 2, 64, 64), torch.float32)
+    keep_w, ws = guarded((K.kda_hla_forward_workspace_size(1, 300, 2, 64, 64, 3, dt),), torch.uint8)
+    K.kda_hla_forward(x["q"], x["k"], x["v"], x["g"], x["S0"], cu_seqlens=c, o=o, S_T=S, workspace=ws)
+    keep_b, wb = guarded((K.kda_hla_backward_workspace_size(1, 300, 2, 64, 64, 3, dt),), torch.uint8)
+    got = K.kda_hla_backward(x["q"], x["k"], x["v"], x["g"], x["do"], x["S0"], x["dS_T"], cu_seqlens=c, workspace=wb)
+    torch.cuda.synchronize()
+    for whole in (keep_o, keep_s, keep_w, keep_b):
+        assert (whole[:GUARD] == 0x5a).all() and (whole[-GUARD:] == 0x5a).all()
+    o2, S2 = K.kda_hla_forward(x["q"], x["k"], x["v"], x["g"], x["S0"], cu_seqlens=c2)
+    want = K.kda_hla_backward(x["q"], x["k"], x["v"], x["g"], x["do"], x["S0"], x["dS_T"], cu_seqlens=c2)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
