@@ -477,13 +477,19 @@ int kda_decode_multi(const void *q, const void *k, const void *v, const void *g,
  *            time.
  *   dev_status : NULL, or a device int set to KDA_ERR_TIMEOUT if a bounded
  *            wait of a tensor-core kernel gives up.
- *   path   : KDA_PATH_AUTO, KDA_PATH_SIMT (CUDA cores) or KDA_PATH_TC (tensor
- *            cores; bf16 only, else KDA_ERR_UNSUPPORTED). AUTO takes the tensor
- *            cores for bf16.
+ *   path   : KDA_PATH_AUTO, KDA_PATH_SIMT (fp32 accuracy, either dtype) or
+ *            KDA_PATH_TC (bf16 products; bf16 only, else KDA_ERR_UNSUPPORTED).
+ *            AUTO takes TC for bf16 and SIMT for fp32.
  *
- * Arithmetic: sums, states and decays in fp32 (the decays' sums in 64 bits). The
- * tensor cores take the scores and the states as bf16 operands; the states
- * themselves are carried in fp32, to about 2^-18. A NaN or an infinity among
+ * Arithmetic: sums, states and decays are held in fp32 (the decays' sums in 64
+ * bits). SIMT takes its products on warp-level TF32 instructions, every operand
+ * as the sum of two TF32 numbers (22 bits): results are off by 2e-7 to 5e-7,
+ * normwise, before their rounding to dtype. TC takes the scores and the states
+ * as bf16 operands (up to 2^-8 each): o and the gradients are off by 2.3e-3 to
+ * 2.8e-3 where their own rounding to bf16 is 1.7e-3; and what is added to a
+ * state as the sum of two bf16 numbers: S_T and dS0 are off by 2.5e-6. dg is a
+ * sum over pairs of a write before the token and a read from it on, so that it
+ * keeps this accuracy however strong the decays are. A NaN or an infinity among
  * q, k, v or dO may reach any row of its chunk (128 tokens on the tensor cores,
  * else 64), earlier ones too, and what follows from the state; other sequences
  * and heads, and rows of no sequence, are not touched by it.

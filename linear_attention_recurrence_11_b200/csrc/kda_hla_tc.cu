@@ -8,8 +8,9 @@
 //
 // Roundings to bf16: the masked scores (as the operand of the second product), the states (as an
 // operand; they are carried in fp32), and the results. The state's own update multiplies k v^T by a
-// decay per token; that product is taken as the sum of two bf16 numbers (hi + lo, 16 bits of the 24),
-// so that the fp32 state is good to about 2^-18 and not to 2^-9.
+// decay per token; that product is taken as the sum of two bf16 numbers (hi + lo, 16 bits of the 24:
+// at most 2^-16 of it is lost, where one number would lose up to 2^-8). The fp32 states and their gradients
+// are off by 2.5e-6 for that, normwise; the products' own sums, by 1.2e-7.
 #include "kda_hla.cuh"
 #include "kda_hla_gate.cuh"
 #include "kda_sm100.cuh"
@@ -93,8 +94,10 @@ struct DecayRow {
 //   warps 8-15   the state: update, operand copy; the outputs: rows of Q S scaled, result stored
 //   warp 16      issues the products: Q K^T; Q S; b^T hi + b^T lo; (scores) V onto the scaled Q S
 //   warp 17      the copies: a tile is requested again as soon as the last product that reads it is done
-// Measured for d = 128: a chunk with outputs 3.3 us (96 heads x 8192 tokens: 210 us; 4600 clocks, of which shared memory
-// is busy for 4500: 96 KB copied in, 96 read and 96 written by the threads, 290 read by the products), a chunk's states
+// Measured for d = 128: a chunk with outputs 3.3 us (96 heads x 8192 tokens: 210 us), 5800 clocks. By its bytes (96 KB
+// copied in, 96 read and 96 written by the threads, 290 read by the products) shared memory is busy for 4500 of them, and
+// every role waits for the others for a third: the operand warps 1700 to 2700 clocks (most of it for the next tiles of a and
+// the gates, whose places are single), the state warps 2000, the issuing thread 2000. A chunk's states
 // 2.3 us with all SMs at it (6.4 TB/s) and 1.9 us with 96, an end state 2.0 us.
 enum { kOut = 0, kStates = 1, kEnds = 2 };
 // 5 warpgroups launched at 96 registers a thread, 480 in all: two go down to 88, two up to 120, the last down to 64
@@ -554,7 +557,7 @@ struct TileArgs {
 // q . dQ2) and what R sees of the writes (k . dK2) while those products are scaled.
 // (The pairs' sums take 10 us of 687 for 96 heads x 8192 tokens; held back until the products of dQ and dK run, whose time
 // they would share, they cost spills and 70 us.)
-// Measured for d = 128: 9.4 us a tile, 96 heads x 8192 tokens 393 us (4.6 TB/s of its 288 KB a tile; 6.6 us at the rate
+// Measured for d = 128: 10.0 us a tile, 74 heads x 8192 tokens 319 us (4.3 TB/s of its 288 KB a tile; 6.6 us at the rate
 // of a copy). The phases of a tile follow each other; warps of their own for copies, products and results took longer.
 template <int DKP, int DVP>
 struct GradTile {

@@ -8,7 +8,7 @@
 // computed once, into shared memory, and used by every head. The angle is reduced in fp64, as
 // p * (inv_freq / 2 pi) minus its nearest integer, so that positions of millions keep fp32's full
 // precision; sine and cosine are then taken of at most half a turn, for bf16 by the special-function
-// unit (2^-21 of a pair's length, where a result's own rounding is 2^-9).
+// unit (2^-21 of a pair's length, where a result's own rounding is up to 2^-8).
 //
 // Two forms. Where pairs stay within a 16-byte vector (interleaved) or their halves divide into vectors of 16 or 8
 // bytes, a thread turns whole vectors in registers. Else (an odd number of pairs, say) the rows are staged in shared

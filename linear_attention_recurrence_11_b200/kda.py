@@ -687,7 +687,8 @@ def kda_hla_forward(q, k, v, g, S0=None, *, scale: float = 1.0, cu_seqlens=None,
     """Chunked prefill of linear attention with one decay per head: ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``,
     ``o_t = scale S_t^T q_t``. q, k ``[B, T, H, dk]``; v ``[B, T, H, dv]`` (fp32 or bf16); g ``[B, T, H]`` of the same
     type, or fp32 ``[H]``; S0 ``[N, H, dv, dk]`` fp32 or None; cu_seqlens int32 ``[N+1]`` (B must be 1) or None.
-    Returns ``(o, S_T)`` (S_T None when ``return_state`` is False and none is given)."""
+    Returns ``(o, S_T)`` (S_T None when ``return_state`` is False and none is given). ``path``: "auto" takes bf16 on the
+    tensor cores with bf16 operands; "simt" has fp32 accuracy for both types (include/kda.h gives figures)."""
     dtype, dev, B, T, H, dk, dv, gate, N = _hla_shapes(q, k, v, g, cu_seqlens)
     if S0 is not None:
         _check(S0, "S0", torch.float32, (N, H, dv, dk), dev)
