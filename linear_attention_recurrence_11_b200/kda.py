@@ -581,6 +581,7 @@ def kda_kcp_scan(S0, M, Z, *, stream=None):
 # (_need only says what is wrong with it), no context manager on the current device, plain integers as pointers, sizes as
 # arguments of torch.empty (a tuple of them costs it a microsecond more).
 _NO_SIZE = ctypes.c_size_t(-1).value
+_INT_MAX = 0x7fffffff  # of the library's sizes: a larger one would arrive as its lowest 32 bits
 _NO_CONTEXT = contextlib.nullcontext()
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -636,6 +637,8 @@ def _hla_first(k, v, dims):
 def _hla_shapes(q, k, v, g, cu_seqlens):
     dtype, dev, dv = _hla_first(k, v, 4)
     B, T, H, dk = k.shape
+    if max(B, T, H, dk, dv) > _INT_MAX:  # (a decode step's state does not fit into the GPU then)
+        raise KdaError(KDA_ERR_UNSUPPORTED, "linear attention")
     _check(q, "q", dtype, (B, T, H, dk), dev)
     _check(v, "v", dtype, (B, T, H, dv), dev)
     gate = _hla_gate(g, dtype, (B, T, H), dev)
@@ -823,8 +826,6 @@ def kda_rope(q, k, inv_freq, *, positions=None, interleaved: bool = False, mscal
     if q.dim() != 4:
         raise ValueError("q is [B, T, H, d]")
     B, T, Hq, d = q.shape
-    if B > 0x7fffffff or T > 0x7fffffff:  # (more than the library's integers hold)
-        raise KdaError(KDA_ERR_UNSUPPORTED, "kda_rope")
     Hk = 0
     if k is not None:
         _need(k, "k", dtype, None, dev)
@@ -836,6 +837,8 @@ def kda_rope(q, k, inv_freq, *, positions=None, interleaved: bool = False, mscal
     _need(inv_freq, "inv_freq", torch.float32, None, dev)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq is [rot_dim / 2]")
+    if max(B, T, Hq, Hk, d, 2 * inv_freq.numel()) > _INT_MAX:
+        raise KdaError(KDA_ERR_UNSUPPORTED, "kda_rope")
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
             raise ValueError("positions is a tensor of int32 or int64")
